@@ -383,6 +383,175 @@ fa_status_t fa_bwd_strided(const void* q, const void* k, const void* v, const vo
                            fa_dtype_t dtype, void* workspace, size_t workspace_bytes,
                            cudaStream_t stream);
 
+/*
+ * What a serving step needs around paged attention, and a training step beside
+ * it.  None of these calls has a counterpart on the attention pages; the
+ * formulas stand here.
+ *
+ * fa_paged_slots -- the arrays of one step from its request lengths, on the
+ * device: offsets, positions, slots and new block-table entries, in one launch.
+ *   past_k[s]   tokens request s holds in the cache; new_q[s]: tokens it adds.
+ *   free_pages  [n_free] page ids to hand out, taken from the front in order
+ *               of the requests (may be NULL when n_free is 0).
+ *   block_table [n_seqs, max_pages_per_seq], read and written: entries of the
+ *               pages a request already holds are read, the entries of the
+ *               pages it newly needs are written, all others are left alone.
+ * With cap = max_pages_per_seq * page_size, past = clamp(past_k, 0, cap),
+ * new = max(new_q, 0), held = min(past + new, cap):
+ *   cu_seqlens_q [n_seqs + 1]  running sum of new, clipped to total_q
+ *   seqused_k    [n_seqs]      held
+ *   block_table                entries ceil(past / page_size) up to
+ *                              ceil(held / page_size) of each request: the next
+ *                              free pages, or -1 once the list has run out
+ *   positions    [total_q]     past + t - cu_seqlens_q[s] for row t of request s
+ *   slot_map     [total_q]     block_table[s][position / page_size] * page_size
+ *                              + position % page_size; -1 where that entry is
+ *                              negative or the position is not below cap
+ *   pages_taken  [1]           pages needed (above n_free: the list ran out)
+ * Rows of no request (total_q may be a padded count) get position 0, slot -1.
+ * The page size is any >= 1; n_seqs <= FA_SLOTS_MAX_SEQS and n_seqs *
+ * max_pages_per_seq < 2^31 (FA_ERR_UNSUPPORTED above).  Outputs must not
+ * overlap inputs (block_table apart): FA_ERR_INVALID_ARG where they do.
+ * total_q = 0 still writes the per-request outputs.
+ */
+#define FA_SLOTS_MAX_SEQS 16384
+
+fa_status_t fa_paged_slots(const int32_t* past_k, const int32_t* new_q, const int32_t* free_pages,
+                           int64_t n_free, int32_t* block_table, int64_t n_seqs,
+                           int64_t max_pages_per_seq, int64_t page_size, int64_t total_q,
+                           int32_t* cu_seqlens_q, int32_t* seqused_k, int32_t* positions,
+                           int64_t* slot_map, int32_t* pages_taken, cudaStream_t stream);
+
+/*
+ * fa_qk_norm_rope -- RMS norm of every query and key head and the rotation by
+ * position, in one pass: for each head vector x of D elements
+ *     u = norm ? x * rsqrt(mean(x^2) + eps) * weight : x
+ *     y = u with its first rot_dim elements rotated in pairs: pair i turns by
+ *         angle positions[axis(i)][b, s] * inv_freq[i]
+ *         (a, b) -> (a cos - b sin, b cos + a sin)
+ * Pair i is elements (i, i + rot_dim / 2), or (2 i, 2 i + 1) with `interleaved`.
+ *   q [B, H, S, D], k [B, H_kv, S, D] with strides[0..1]; q_out, k_out with
+ *     strides[2..3] (fa_strides_t as above; an output may be its input's
+ *     memory when the strides are equal too, and must not overlap it
+ *     otherwise).
+ *   q_weight, k_weight: [D] in `dtype`, or NULL for ones; NULL without `norm`.
+ *   positions: int32 [n_axes, B, S], any value of the type; n_axes 1..4.
+ *   inv_freq: double [rot_dim / 2], radians a position (a device array).
+ *     The angle is reduced modulo a turn in 64-bit integers, so that it is as
+ *     exact at position 2^31 as at 1; a frequency that is not finite reads as 0.
+ *   pair_axis: HOST array [rot_dim / 2] of axes, each < n_axes; NULL: all 0.
+ *   rot_dim: 0 (norm only; positions and inv_freq may be NULL) or a multiple
+ *     of 16 up to D.  norm = 0 with rot_dim = 0 is FA_ERR_INVALID_ARG.
+ *   dtype: FA_DTYPE_F16 or FA_DTYPE_BF16; D 64 or 128.  fp32 arithmetic, one
+ *     rounding.  B * S = 0 returns FA_OK.
+ * eps finite and >= 0.  One launch.
+ *
+ * fa_qk_norm_rope_bwd -- its gradients.  With g = dy turned back, r =
+ * rsqrt(mean(x^2) + eps), h = x r:
+ *     dweight = sum g h,    dx = r (g w - h mean(g w h))     (norm)
+ *     dx = g                                                  (no norm)
+ *   dq_out, dk_out: gradients of the outputs; q, k: the forward's inputs (not
+ *   read, and may be NULL, without norm); dq, dk: written; strides[0..5] =
+ *   dq_out, dk_out, q, k, dq, dk.  dq / dk may be dq_out / dk_out (same
+ *   strides).  dq_weight, dk_weight: [D] in `dtype`, written; NULL: not
+ *   wanted.  workspace: fa_qk_norm_rope_bwd_workspace_size bytes, 256-byte
+ *   aligned, contents irrelevant; may be NULL when neither weight gradient is
+ *   wanted.  Deterministic (no atomics).  B * S = 0 writes zero weight
+ *   gradients.  Up to two launches; calls sharing a workspace must not overlap.
+ */
+fa_status_t fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
+                            const void* q_weight, const void* k_weight, const int32_t* positions,
+                            const double* inv_freq, int64_t B, int64_t S, int64_t H, int64_t H_kv,
+                            int64_t D, int64_t rot_dim, int64_t n_axes, const uint8_t* pair_axis,
+                            int interleaved, int norm, float eps, const fa_strides_t* strides,
+                            fa_dtype_t dtype, cudaStream_t stream);
+
+fa_status_t fa_qk_norm_rope_bwd_workspace_size(int64_t D, size_t* workspace_bytes);
+
+fa_status_t fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q,
+                                const void* k, void* dq, void* dk, const void* q_weight,
+                                const void* k_weight, void* dq_weight, void* dk_weight,
+                                const int32_t* positions, const double* inv_freq, int64_t B,
+                                int64_t S, int64_t H, int64_t H_kv, int64_t D, int64_t rot_dim,
+                                int64_t n_axes, const uint8_t* pair_axis, int interleaved, int norm,
+                                float eps, const fa_strides_t* strides, fa_dtype_t dtype,
+                                void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * A paged K/V cache of 4-bit values.  Each of K and V is
+ *     codes  uint8 [num_pages, H_kv, page_size, D / 2]
+ *     scales uint8 [num_pages, H_kv, page_size, D / 16]
+ * codes: OCP E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two a byte,
+ * the even element in the low nibble; scales: OCP E4M3 ("fn"), one for 16
+ * elements along D; and one fp32 descale a tensor:
+ *     value = code * scale * descale            (9/16 byte an element)
+ * The head is outside the row so that the rows of one head of one page, what an
+ * attention work item reads, are one run of memory.  A scale's NaN code, which
+ * fa_kv4_write never makes, reads as NaN (and may reach the neighbours of the
+ * sequence that holds it); nothing else makes a value NaN or infinite.
+ * descale_k, descale_v are host floats in [2^-100, 2^100] (FA_ERR_INVALID_ARG
+ * outside).  D 64 or 128; codes and scales 16-byte aligned; page sizes
+ * as fa_fwd_paged.
+ *
+ * fa_kv4_write -- rows of k and v into slots: row t goes to slot slot_map[t],
+ *   page slot / page_size, row slot % page_size.  k, v: [n_tokens, H_kv, D] in
+ *   `dtype` (F16 or BF16) with element strides strides[0..1].seq and .head
+ *   (.batch is not used).  Slots outside [0, num_pages * page_size) are skipped
+ *   (padding); the others have to differ from one another -- a slot named twice
+ *   holds a mixture of the rows.  Each group's scale is the e4m3 value nearest
+ *   to max|x| / (6 descale) (at most 448; even on ties), each code the e2m1
+ *   value nearest to x / (scale descale), ties to even, saturated at 6; all as
+ *   if computed exactly.  A group whose scale rounds to 0 is all zeros.  NaN
+ *   becomes code +-6 and does not count for the maximum; infinities give scale
+ *   448.  n_tokens = 0 returns FA_OK.  One launch.
+ * fa_kv4_read -- the reverse: rows k_out, v_out [n_tokens, H_kv, D] (dense, in
+ *   `dtype`) of the slots; a slot outside the cache reads as zeros, a slot may
+ *   be named any number of times.  Rounded once, to nearest even.
+ */
+fa_status_t fa_kv4_write(const void* k, const void* v, const int64_t* slot_map, uint8_t* k_codes,
+                         uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales, float descale_k,
+                         float descale_v, int64_t n_tokens, int64_t H_kv, int64_t D,
+                         int64_t page_size, int64_t num_pages, const fa_strides_t* strides,
+                         fa_dtype_t dtype, cudaStream_t stream);
+
+fa_status_t fa_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                        const uint8_t* v_scales, const int64_t* slot_map, void* k_out, void* v_out,
+                        float descale_k, float descale_v, int64_t n_tokens, int64_t H_kv, int64_t D,
+                        int64_t page_size, int64_t num_pages, fa_dtype_t dtype,
+                        cudaStream_t stream);
+
+/*
+ * fa_fwd_paged_kv4 -- attention of packed queries over the 4-bit cache: q, o,
+ *   lse, cu_seqlens_q, seqused_k, block_table, causal and a row without keys
+ *   (O = 0, lse = -inf) as fa_fwd_paged; the cache and its descales as above.
+ *   dtype: F16 or BF16 (of q and o).  Keys behind seqused_k are not looked at;
+ *   pages outside [0, num_pages) read as zeros.
+ *   Where max_seqlen_q * H / H_kv is small (decoding, a few speculative
+ *   tokens) the cache is read as it is, its work split evenly over the GPU
+ *   whatever the lengths; otherwise the keys and values of the sequences that
+ *   bring queries are unpacked into the workspace (V with its descale, one
+ *   rounding to `dtype`) and the dense tensor-core forward reads them there.
+ *   total_k: at least the sum of seqused_k (host-known; it sizes the unpacked
+ *   rows; keys past it may be left out).  At most 16384 sequences when
+ *   unpacking.
+ *   workspace: at least fa_fwd_paged_kv4_workspace_size bytes, 256-byte
+ *   aligned, contents irrelevant.  Two launches; calls sharing a workspace
+ *   must not overlap.  Deterministic (no atomics).
+ */
+fa_status_t fa_fwd_paged_kv4_workspace_size(int64_t n_seqs, int64_t max_seqlen_q, int64_t total_k,
+                                            int64_t H, int64_t H_kv, int64_t D,
+                                            size_t* workspace_bytes);
+
+fa_status_t fa_fwd_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_t* k_scales,
+                             const uint8_t* v_codes, const uint8_t* v_scales, void* o, float* lse,
+                             const int32_t* cu_seqlens_q, const int32_t* seqused_k,
+                             const int32_t* block_table, int64_t n_seqs, int64_t max_pages_per_seq,
+                             int64_t page_size, int64_t num_pages, int64_t total_q,
+                             int64_t max_seqlen_q, int64_t total_k, int64_t H, int64_t H_kv,
+                             int64_t D, float scale, int causal, fa_dtype_t dtype, float descale_k,
+                             float descale_v, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream);
+
 /* A static, human-readable name for a status code (never NULL). */
 const char* fa_status_string(fa_status_t s);
 

@@ -1,0 +1,418 @@
+"""The 4-bit cache: kv4_write and kv4_read against the exact reference (codes and scales bit by
+bit), and attention over it against 64-bit attention within bounds from its arithmetic."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+import tiled_attention_10_gb300 as fa
+from tests import paged_reference as ref
+from tests.gpu_helpers import CANARY16, CANARY32
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def raw(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def junk_cache(pages, ps, H_kv, D, kd=1.0, vd=1.0, fill=0xA5):
+    c = fa.KV4Cache.allocate(pages, ps, H_kv, D, k_descale=kd, v_descale=vd)
+    for t in (c.k_codes, c.k_scales, c.v_codes, c.v_scales):
+        t.view(torch.uint8).fill_(fill)
+    return c
+
+
+def check_written(cache, k, v, slots, before):
+    """Every byte of the cache: written rows by the rule, all others as before."""
+    for x, codes, scales, d, old in ((k, cache.k_codes, cache.k_scales, cache.k_descale, before[0]),
+                                     (v, cache.v_codes, cache.v_scales, cache.v_descale, before[1])):
+        want_c, want_s = old[0].copy(), old[1].copy()
+        c, s = ref.to_cache(np64(x), d)
+        ps = cache.page_size
+        for t, slot in enumerate(slots):
+            if 0 <= slot < cache.num_pages * ps:
+                want_c[slot // ps, :, slot % ps] = c[t]
+                want_s[slot // ps, :, slot % ps] = s[t]
+        assert np.array_equal(want_s, raw(scales))
+        assert np.array_equal(want_c, raw(codes))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("n,H_kv,D,ps,pages", [(1, 1, 64, 16, 1), (3, 2, 128, 16, 4), (70, 8, 128, 64, 3), (257, 3, 64, 32, 20),
+                                               (129, 1, 128, 128, 2), (400, 2, 64, 384, 3), (33, 5, 128, 256, 2)])
+def test_write_and_read(cuda_lib, dtype, n, H_kv, D, ps, pages):
+    g = torch.Generator().manual_seed(n)
+    cache = junk_cache(pages, ps, H_kv, D, 0.0024, 0.7e-3)
+    before = [(raw(a).copy(), raw(b).copy()) for a, b in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales))]
+    x = torch.randn(n, 3 * H_kv, D, generator=g).to(DT[dtype]).cuda()
+    k, v = x[:, :H_kv], x[:, 2 * H_kv:]                # strided rows
+    slots = torch.randperm(pages * ps, generator=g)[:n]
+    slots = torch.cat((slots, torch.full((n - len(slots),), -1)))
+    slots[::7] = -1
+    if n > 5:
+        slots[3], slots[5] = pages * ps, -(2 ** 40)     # outside: skipped
+    fa.kv4_write(k, v, slots.cuda(), cache)
+    check_written(cache, k, v, slots.tolist(), before)
+    got = fa.kv4_read(cache, slots.cuda(), dtype=DT[dtype])
+    for x, y, d, codes, scales in ((k, got[0], cache.k_descale, cache.k_codes, cache.k_scales),
+                                   (v, got[1], cache.v_descale, cache.v_codes, cache.v_scales)):
+        c, s = ref.to_cache(np64(x), d)
+        want = ref.values(c, s, d)
+        ok = ((slots >= 0) & (slots < pages * ps)).numpy()
+        want[~ok] = 0.0
+        # fp32 product, then one rounding
+        assert (np.abs(np64(y) - want) <= ref.half_step(DT[dtype]) * 1.001 * np.abs(want) + ref.tiny(DT[dtype])).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("descale", [1.0, 2.0 ** -9, 6.5 * 0.7 / 2688, 0.3, 1e-20, 1e20])
+def test_borders_between_codes(cuda_lib, dtype, descale):
+    """Values on, and one step beside, every border between codes and between scales."""
+    dt = DT[dtype]
+    d32 = float(np.float32(descale))
+    rows = []
+    for s in ref.e4m3_values()[[1, 2, 7, 8, 9, 15, 40, 41, 47, 86, 87, 100, 120, 126]]:
+        for near in (1.0, 0.999, 1.0625, 1.0624, 1.0626):         # the group's largest: on the scale's borders too
+            for b in (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 5.99):
+                rows.append([6 * s * d32 * near] + [b * s * d32 * (1 + j * 2.0 ** -9) * (-1) ** j for j in range(-7, 8)])
+    x = torch.tensor(rows, dtype=torch.float64).to(dt)
+    x = torch.cat((x, torch.zeros((-len(x)) % 4, 16, dtype=dt))).view(-1, 1, 64).cuda()
+    cache = junk_cache(-(-len(x) // 16), 16, 1, 64, descale, descale)
+    before = [(raw(a).copy(), raw(b).copy()) for a, b in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales))]
+    slots = torch.arange(len(x), device="cuda")
+    fa.kv4_write(x, x.flip(0), slots, cache)
+    check_written(cache, x, x.flip(0), slots.tolist(), before)
+
+
+def test_every_bf16_value(cuda_lib):
+    """All 65536 bit patterns, NaN and infinities among them, as elements of random groups."""
+    bits = torch.randperm(65536, generator=torch.Generator().manual_seed(1)).to(torch.int32).to(torch.int16)
+    x = bits.view(torch.bfloat16).view(-1, 8, 64).cuda()
+    for d in (1.0, 1e-6):
+        cache = junk_cache(8, 16, 8, 64, d, d)
+        before = [(raw(a).copy(), raw(b).copy()) for a, b in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales))]
+        fa.kv4_write(x, x, torch.arange(128, device="cuda"), cache)
+        check_written(cache, x, x, list(range(128)), before)
+
+
+def test_read_nan_scale_and_duplicates(cuda_lib):
+    cache = junk_cache(1, 16, 1, 64, fill=0x11)
+    cache.k_scales.view(torch.uint8)[0, 0, 3, 2] = 0x7F
+    k, v = fa.kv4_read(cache, torch.tensor([3, 3, 99, 0], device="cuda"))
+    assert torch.isnan(k[:2, 0, 32:48]).all() and torch.isfinite(k[:2, 0, :32]).all() and torch.equal(v[0], v[1])
+    assert (k[2] == 0).all() and torch.isfinite(k[3]).all()
+
+
+# ---------------------------------------------------------------- attention
+class Step:
+    """A paged step with a cache of written values, junk behind every sequence's last key."""
+
+    def __init__(self, seq_q, seq_k, H, H_kv, D, ps, dtype, seed=0, std=1.0, kd=0.003, vd=0.002, extra_rows=0, bad_page=False):
+        g = torch.Generator().manual_seed(seed)
+        self.seq_q, self.seq_k, self.H, self.H_kv, self.D, self.dtype = seq_q, seq_k, H, H_kv, D, DT[dtype]
+        per = [-(-n // ps) for n in seq_k]
+        pages = max(1, sum(per)) + 2
+        self.cache = junk_cache(pages, ps, H_kv, D, kd, vd, fill=0x7F)     # unwritten scales are NaN
+        order = torch.randperm(pages, generator=g)
+        cols = max(1, max(per)) + 1
+        table = torch.full((len(seq_k), cols), 2 ** 31 - 1, dtype=torch.int32)
+        at = 0
+        for s, n in enumerate(per):
+            table[s, :n] = order[at:at + n].int()
+            at += n
+        slots = [int(table[s, j // ps]) * ps + j % ps for s, n in enumerate(seq_k) for j in range(n)]
+        tk = sum(seq_k)
+        k = (torch.randn(tk, H_kv, D, generator=g) * std).to(self.dtype).cuda()
+        v = torch.randn(tk, H_kv, D, generator=g).to(self.dtype).cuda()
+        if tk:
+            fa.kv4_write(k, v, torch.tensor(slots).cuda(), self.cache)
+        if bad_page:
+            table[0, 0] = -1
+        self.table = table.cuda()
+        self.used = torch.tensor(seq_k, dtype=torch.int32).cuda()
+        self.cu = torch.tensor([0, *itertools.accumulate(seq_q)], dtype=torch.int32).cuda()
+        self.tq = sum(seq_q) + extra_rows
+        self.q = torch.randn(self.tq, H, D, generator=g).to(self.dtype).cuda()
+
+    def run(self, causal=2, scale=None, max_q=None, **kw):
+        o = torch.full((self.tq, self.H, self.D), CANARY16, dtype=torch.int16, device="cuda").view(self.dtype)
+        lse = torch.full((self.H, self.tq), CANARY32, dtype=torch.int32, device="cuda").view(torch.float32)
+        fa.paged_attention_kv4(self.q, self.cache, self.cu, self.used, self.table, max_seqlen_q=max_q or max(1, *self.seq_q),
+                               total_k=sum(self.seq_k), scale=scale, causal=causal, out=o, lse=lse, **kw)
+        return o, lse
+
+    def check(self, o, lse, causal=2, scale=None, unpacked=None):
+        scale = self.D ** -0.5 if scale is None else scale
+        c = self.cache
+        arrays = [(raw(a), raw(b), d) for a, b, d in ((c.k_codes, c.k_scales, c.k_descale), (c.v_codes, c.v_scales, c.v_descale))]
+        table, q64, o64, l64 = self.table.cpu().numpy(), np64(self.q), np64(o), np64(lse)
+        if unpacked is None:
+            unpacked = max(1, *self.seq_q) * (self.H // self.H_kv) > 64
+        at = 0
+        for s, (nq, nk) in enumerate(zip(self.seq_q, self.seq_k)):
+            k, v = (ref.gather(*a, table[s], nk, c.num_pages) for a in arrays)
+            O, L, PV, A = ref.attend(q64[at:at + nq], k, v, scale, causal)
+            half = ref.half_step(self.dtype)
+            p_step, v_step = (half, half) if unpacked else (ref.half_step(torch.float16), 0.0)
+            bo, bl = ref.attend_bounds(O, PV, A, nk, self.D, self.dtype, p_step, v_step)
+            rows = slice(at, at + nq)
+            assert np.isfinite(o64[rows]).all()
+            assert (np.abs(o64[rows] - O) <= bo).all(), (s, (np.abs(o64[rows] - O) / bo).max())
+            assert np.array_equal(np.isneginf(L), np.isneginf(l64[:, rows]))
+            fin = np.isfinite(L)
+            assert (np.abs(l64[:, rows] - L)[fin] <= bl[fin]).all()
+            at += nq
+        # rows of no sequence: untouched
+        assert (o[at:].view(torch.int16) == CANARY16).all() and (lse[:, at:].contiguous().view(torch.int32) == CANARY32).all()
+
+
+HEADS = [(1, 1), (4, 1), (8, 8), (12, 4), (28, 4), (16, 1), (8, 1), (5, 1)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("heads", HEADS, ids=str)
+def test_decode(cuda_lib, heads, dtype, D):
+    st = Step([1, 0, 1, 1, 1, 1, 1, 0], [1, 50, 17, 300, 64, 65, 0, 0], *heads, D, 16, dtype, seed=heads[0], extra_rows=3)
+    st.check(*st.run())
+
+
+@pytest.mark.parametrize("ps", [16, 32, 64, 128, 256, 384])
+def test_decode_page_sizes(cuda_lib, ps):
+    st = Step([1] * 5, [ps - 1, ps, ps + 1, 3 * ps + 7, 1000], 8, 2, 128, ps, "bf16", seed=ps)
+    st.check(*st.run())
+
+
+@pytest.mark.parametrize("n", [1, 15, 16, 31, 32, 33, 63, 64, 127, 128, 129, 255, 257, 4097, 20000])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_lengths(cuda_lib, n, D):
+    st = Step([1], [n], 4, 2, D, 64, "bf16", seed=n)
+    st.check(*st.run())
+
+
+@pytest.mark.parametrize("causal", [0, 1, 2])
+@pytest.mark.parametrize("qmax,heads", [(2, (8, 2)), (4, (4, 1)), (5, (3, 1)), (8, (8, 1)), (16, (8, 2)), (64, (2, 2)), (7, (28, 4))], ids=str)
+def test_several_queries(cuda_lib, qmax, heads, causal):
+    st = Step([qmax, 1, 0, qmax - 1, qmax], [200, 3, 40, qmax - 1, max(1, qmax - 2)], *heads, 128, 32, "bf16", seed=qmax, extra_rows=2)
+    st.check(*st.run(causal), causal)
+
+
+@pytest.mark.parametrize("causal", [0, 1, 2])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64), ("f16", 128), ("bf16", 64)])
+def test_long_queries_are_unpacked(cuda_lib, dtype, D, causal):
+    st = Step([130, 1, 0, 70, 300], [500, 33, 64, 20, 300], 4, 2, D, 16, dtype, seed=D, extra_rows=5)
+    st.check(*st.run(causal), causal)
+
+
+def test_both_ways_agree_at_the_border(cuda_lib):
+    """The same queries through the cache as it is and, with a larger max_seqlen_q, unpacked."""
+    st = Step([8, 3], [700, 90], 8, 2, 128, 64, "bf16", seed=3)
+    st.check(*st.run())
+    st.check(*st.run(max_q=100), unpacked=True)
+
+
+@pytest.mark.parametrize("scale", [-0.08, 0.0, 1.0, 3.0])
+@pytest.mark.parametrize("qn", [1, 40])
+def test_scales(cuda_lib, scale, qn):
+    st = Step([qn, qn], [900, 333], 4, 2, 128, 16, "bf16", seed=4)
+    st.check(*st.run(scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("std,mul", [(30.0, 1.0), (1.0, 1e-30), (1.0, 1e30), (1e-3, 1.0)])
+def test_magnitudes(cuda_lib, std, mul):
+    """Peaked and flat softmax; queries far outside f16's range, undone by the scale."""
+    st = Step([1, 1, 2], [700, 64, 90], 4, 1, 128, 32, "bf16", seed=5, std=std, kd=0.003 * std)
+    st.q.mul_(mul)
+    scale = 128 ** -0.5 / mul
+    st.check(*st.run(scale=scale), scale=scale)
+
+
+def test_pages_outside_the_cache_read_as_zeros(cuda_lib):
+    for qn in (1, 40):
+        st = Step([qn, qn], [100, 70], 4, 2, 128, 16, "bf16", seed=6, bad_page=True)
+        st.check(*st.run())
+
+
+def test_bad_offsets_stay_inside(cuda_lib):
+    """Offsets and lengths that no caller should give: nothing outside o and lse is written."""
+    st = Step([1, 1, 1], [40, 50, 60], 4, 2, 64, 16, "bf16", seed=7)
+    good = st.run()
+    st.used[1] = -5
+    st.used[2] = 2 ** 31 - 1
+    st.cu.copy_(torch.tensor([0, 1, 2 ** 31 - 1, -7], dtype=torch.int32))
+    o, lse = st.run()
+    assert torch.equal(o[0], good[0][0])
+    assert torch.isneginf(lse[:, 1]).all() and (o[1] == 0).all()
+
+
+@pytest.mark.parametrize("lens", [[30000], [20000, 1, 1, 1], [513] * 40, list(range(1, 200, 3)), [64] * 700])
+def test_any_split_of_the_work(cuda_lib, lens):
+    st = Step([1] * len(lens), lens, 8, 4, 64, 16, "f16", seed=8)
+    o, lse = st.run()
+    st.check(o, lse)
+    again = st.run()
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])       # deterministic
+
+
+def test_a_sequences_result_does_not_depend_on_rows_behind(cuda_lib):
+    """The same step with a longer table, padded requests and an unordered workspace."""
+    st = Step([1, 1], [300, 200], 4, 2, 128, 16, "bf16", seed=9)
+    st.check(*st.run())
+    ws = fa.paged_attention_kv4_workspace(st.q, st.cache, max_seqlen_q=1, n_seqs=2, total_k=500)
+    ws.fill_(0xFF)
+    a = st.run(workspace=ws)
+    st.used = torch.cat((st.used, torch.tensor([70, 0], dtype=torch.int32, device="cuda")))
+    st.cu = torch.cat((st.cu, st.cu[-1:].repeat(2)))
+    st.table = torch.cat((st.table, torch.full_like(st.table, -1)))
+    b = st.run(workspace=ws)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_cache_past_32_bit_offsets(cuda_lib):
+    """Pages whose codes and scales start beyond 2^32 bytes."""
+    pages, ps = (1 << 32) // (64 * 16) + 300, 16
+    pages = pages * 8 + 64                                # the scales' offsets as well: 38 GB of codes each
+    c = fa.KV4Cache(*(torch.empty(pages, 1, ps, n, dtype=torch.uint8, device="cuda") for n in (64, 8, 64, 8)), 0.003, 0.003)
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(50, 1, 128, generator=g).bfloat16().cuda() for _ in range(2))
+    table = torch.tensor([[pages - 1, 7, pages - 9, pages // 2 + 1]], dtype=torch.int32)
+    slots = torch.tensor([int(table[0, j // ps]) * ps + j % ps for j in range(50)]).cuda()
+    fa.kv4_write(k, v, slots, c)
+    rk, rv = fa.kv4_read(c, slots)
+    small = fa.KV4Cache.allocate(4, ps, 1, 128, k_descale=0.003, v_descale=0.003)
+    fa.kv4_write(k, v, torch.arange(50, device="cuda"), small)
+    sk, sv = fa.kv4_read(small, torch.arange(50, device="cuda"))
+    assert torch.equal(rk, sk) and torch.equal(rv, sv)
+    used = torch.tensor([50], dtype=torch.int32, device="cuda")
+    for n in (1, 50):
+        q = torch.randn(n, 4, 128, generator=g).bfloat16().cuda()
+        cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        a = fa.paged_attention_kv4(q, c, cu, used, table.cuda(), max_seqlen_q=n, total_k=50)
+        b = fa.paged_attention_kv4(q, small, cu, used, torch.arange(4, dtype=torch.int32, device="cuda").view(1, 4),
+                                   max_seqlen_q=n, total_k=50)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_no_queries_and_no_tokens(cuda_lib):
+    st = Step([0, 0], [20, 0], 4, 2, 64, 16, "bf16")
+    o, lse = fa.paged_attention_kv4(st.q, st.cache, st.cu, st.used, st.table, max_seqlen_q=1, total_k=20)
+    assert o.shape == (0, 4, 64) and lse.shape == (4, 0)
+    none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    slots = torch.empty(0, dtype=torch.int64, device="cuda")
+    before = raw(st.cache.k_codes).copy()
+    fa.kv4_write(none, none, slots, st.cache)
+    assert np.array_equal(before, raw(st.cache.k_codes)) and fa.kv4_read(st.cache, slots)[0].shape == (0, 2, 64)
+
+
+def test_wrapper_refusals(cuda_lib):
+    st = Step([1], [20], 4, 2, 64, 16, "bf16")
+    args = (st.q, st.cache, st.cu, st.used, st.table)
+    for i, bad in ((0, st.q.float()), (0, st.q[:, :, :32].contiguous()), (2, st.cu.long()), (2, st.cu[:-1]), (3, st.used.cpu()),
+                   (4, st.table.long())):
+        a = list(args)
+        a[i] = bad
+        with pytest.raises((TypeError, ValueError)):
+            fa.paged_attention_kv4(*a, max_seqlen_q=1)
+    with pytest.raises(fa.FaError):
+        fa.paged_attention_kv4(*args, max_seqlen_q=1, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        fa.kv4_write(st.q, st.q, torch.zeros(1, dtype=torch.int64, device="cuda"), st.cache)   # 4 heads into 2
+
+
+# ---------------------------------------------------------------- the operators together
+def _serve(steps, H, H_kv, D, ps, dtype, capture=False):
+    """Serving steps of three requests through slots, norm and rotation, write and attention; the
+    last step's outputs and everything a reference needs to redo them from the 16-bit inputs."""
+    g = torch.Generator().manual_seed(11)
+    n, cols = 3, 12
+    freq = (10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)).cuda()
+    w = [(1 + 0.1 * torch.randn(D, generator=g)).to(DT[dtype]).cuda() for _ in range(2)]
+    cache = junk_cache(40, ps, H_kv, D, 0.003, 0.003, fill=0x7F)
+    free = torch.randperm(40, generator=g).int().cuda()
+    table = torch.full((n, cols), -1, dtype=torch.int32, device="cuda")
+    past = torch.zeros(n, dtype=torch.int32, device="cuda")
+    held = [[[], []] for _ in range(n)]
+    for new in steps:
+        rows = sum(new) + 2                                   # two padded rows
+        x = torch.randn(rows, H + 2 * H_kv, D, generator=g).to(DT[dtype]).cuda()
+        sl = fa.paged_slots(past, torch.tensor(new, dtype=torch.int32).cuda(), free, table, page_size=ps, total_q=rows)
+        q, k = fa.qk_norm_rope(x[:, :H], x[:, H:H + H_kv], sl.positions, freq, q_weight=w[0], k_weight=w[1])
+        fa.kv4_write(k, x[:, H + H_kv:], sl.slot_map, cache)
+        o, lse = fa.paged_attention_kv4(q, cache, sl.cu_seqlens_q, sl.seqused_k, table, max_seqlen_q=max(new), total_k=400)
+        at = 0
+        for s, m in enumerate(new):
+            held[s][0].append(np64(k[at:at + m]))
+            held[s][1].append(np64(x[at:at + m, H + H_kv:]))
+            at += m
+        free = free[int(sl.pages_taken):]
+        past = sl.seqused_k
+    return q, o, lse, held, steps[-1], cache
+
+
+@pytest.mark.parametrize("H,H_kv,D,ps,dtype", [(8, 2, 128, 16, "bf16"), (4, 4, 64, 32, "f16")])
+def test_serving_steps_together(cuda_lib, H, H_kv, D, ps, dtype):
+    q, o, lse, held, last, cache = _serve([[70, 5, 33], [1, 1, 1], [1, 0, 4], [1, 1, 1]], H, H_kv, D, ps, dtype)
+    at = 0
+    for s, nq in enumerate(last):
+        kv = [ref.values(*ref.to_cache(np.concatenate(h), d), d).transpose(1, 0, 2)
+              for h, d in zip(held[s], (cache.k_descale, cache.v_descale))]
+        O, L, PV, A = ref.attend(np64(q[at:at + nq]), *kv, D ** -0.5, 2)
+        bo, bl = ref.attend_bounds(O, PV, A, kv[0].shape[1], D, DT[dtype], ref.half_step(torch.float16), 0.0)
+        assert (np.abs(np64(o[at:at + nq]) - O) <= bo).all() and (np.abs(np64(lse[:, at:at + nq]) - L) <= bl).all()
+        at += nq
+
+
+def test_captured_decode_step(cuda_lib):
+    """One graph of the four calls, replayed over growing requests, against the calls made one by one."""
+    H, H_kv, D, ps, n = 8, 2, 128, 16, 4
+    g = torch.Generator().manual_seed(12)
+    freq = (10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)).cuda()
+    x = torch.empty(n, H + 2 * H_kv, D, dtype=torch.bfloat16, device="cuda")
+    one = torch.ones(n, dtype=torch.int32, device="cuda")
+    free = torch.arange(60, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    xs = [torch.randn(x.shape, generator=g).bfloat16().cuda() for _ in range(40)]
+
+    def step(past, table, cache, used_pages):
+        sl = fa.paged_slots(past, one, used_pages, table, page_size=ps, total_q=n)
+        q, k = fa.qk_norm_rope(x[:, :H], x[:, H:H + H_kv], sl.positions, freq)
+        fa.kv4_write(k, x[:, H + H_kv:], sl.slot_map, cache)
+        return sl, fa.paged_attention_kv4(q, cache, sl.cu_seqlens_q, sl.seqused_k, table, max_seqlen_q=1, total_k=400)
+
+    def fresh():
+        return (torch.zeros(n, dtype=torch.int32, device="cuda"), torch.full((n, 8), -1, dtype=torch.int32, device="cuda"),
+                fa.KV4Cache.allocate(60, ps, H_kv, D, k_descale=0.003, v_descale=0.003))
+
+    past, table, cache = fresh()
+    pages = free.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(past, table.clone(), cache, pages)
+    torch.cuda.current_stream().wait_stream(side)
+    cache = fresh()[2]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sl, (o, lse) = step(past, table, cache, pages)
+    taken, got = 0, []
+    for x0 in xs:
+        x.copy_(x0)
+        pages[: 60 - taken].copy_(free[taken:])
+        graph.replay()
+        got.append((o.clone(), lse.clone()))
+        taken += int(sl.pages_taken)
+        past.copy_(sl.seqused_k)
+    past, table, cache = fresh()
+    taken = 0
+    for x0, (a, b) in zip(xs, got):
+        x.copy_(x0)
+        sl2, (o2, l2) = step(past, table, cache, free[taken:])
+        assert torch.equal(a, o2) and torch.equal(b, l2)
+        taken += int(sl2.pages_taken)
+        past = sl2.seqused_k

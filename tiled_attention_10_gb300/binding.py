@@ -19,7 +19,9 @@ FA_STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED",
 
 # Symbols the header declares; the library must export all of them.
 EXPORTS = ("fa_fwd", "fa_fwd_gqa", "fa_fwd_splitkv", "fa_fwd_splitkv_plan", "fa_fwd_splitkv_noalloc", "fa_bwd", "fa_bwd_workspace_size", "fa_fwd_varlen", "fa_fwd_paged", "fa_fwd_paged_split", "fa_fwd_paged_split_workspace_size", "fa_fwd_paged_split_plan", "fa_fwd_strided", "fa_bwd_strided", "fa_status_string", "fa_last_device_error", "fa_set_wait_limit_ns",
-           "fa_probe_wait_timeout", "fa_version")
+           "fa_probe_wait_timeout", "fa_version", "fa_paged_slots", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
+           "fa_qk_norm_rope_bwd_workspace_size", "fa_kv4_write", "fa_kv4_read", "fa_fwd_paged_kv4",
+           "fa_fwd_paged_kv4_workspace_size")
 
 
 
@@ -109,6 +111,22 @@ def load(path: str = LIB_PATH):
     lib.fa_set_wait_limit_ns.restype = None
     lib.fa_probe_wait_timeout.argtypes = [u64, vp]
     lib.fa_probe_wait_timeout.restype = ip
+    lib.fa_paged_slots.argtypes = [vp, vp, vp, i64, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp]
+    lib.fa_paged_slots.restype = ip
+    lib.fa_qk_norm_rope.argtypes = [vp] * 8 + [i64] * 7 + [vp, ip, ip, f32, vp, ip, vp]
+    lib.fa_qk_norm_rope.restype = ip
+    lib.fa_qk_norm_rope_bwd.argtypes = [vp] * 12 + [i64] * 7 + [vp, ip, ip, f32, vp, ip, vp, sz, vp]
+    lib.fa_qk_norm_rope_bwd.restype = ip
+    lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [i64, ctypes.POINTER(sz)]
+    lib.fa_qk_norm_rope_bwd_workspace_size.restype = ip
+    lib.fa_kv4_write.argtypes = [vp] * 7 + [f32, f32] + [i64] * 5 + [vp, ip, vp]
+    lib.fa_kv4_write.restype = ip
+    lib.fa_kv4_read.argtypes = [vp] * 7 + [f32, f32] + [i64] * 5 + [ip, vp]
+    lib.fa_kv4_read.restype = ip
+    lib.fa_fwd_paged_kv4.argtypes = ([vp] * 10 + [i64] * 10 + [f32, ip, ip, f32, f32, vp, sz, vp])
+    lib.fa_fwd_paged_kv4.restype = ip
+    lib.fa_fwd_paged_kv4_workspace_size.argtypes = [i64] * 6 + [ctypes.POINTER(sz)]
+    lib.fa_fwd_paged_kv4_workspace_size.restype = ip
     lib.fa_version.argtypes = []
     lib.fa_version.restype = ctypes.c_char_p
     _lib = lib
@@ -288,6 +306,95 @@ def fa_bwd_strided(q, k, v, o, dout, lse, dq, dk, dv, B, H, H_kv, S_q, S_kv, D, 
     return int(lib.fa_bwd_strided(q, k, v, o, dout, lse, dq, dk, dv, int(B), int(H), int(H_kv),
                                   int(S_q), int(S_kv), int(D), arr, float(scale),
                                   int(bool(causal)), dt, workspace, int(workspace_bytes), stream))
+
+
+def fa_paged_slots(past_k, new_q, free_pages, n_free, block_table, n_seqs, max_pages, page_size,
+                   total_q, cu_q, seqused_k, positions, slot_map, pages_taken, stream=None) -> int:
+    """Block tables, slots, offsets and positions of a paged step (device pointers)."""
+    return int(load().fa_paged_slots(past_k, new_q, free_pages, int(n_free), block_table,
+                                     int(n_seqs), int(max_pages), int(page_size), int(total_q),
+                                     cu_q, seqused_k, positions, slot_map, pages_taken, stream))
+
+
+def _axes_array(pair_axis):
+    return None if pair_axis is None else bytes(pair_axis)
+
+
+def fa_qk_norm_rope(q, k, q_out, k_out, q_weight, k_weight, positions, inv_freq, B, S, H, H_kv, D,
+                    rot_dim, n_axes, pair_axis, interleaved, norm, eps, strides, dtype,
+                    stream=None) -> int:
+    """Norm and rotation of query and key heads: `strides` = four (batch, head,
+    seq) triples for q, k, q_out, k_out; `pair_axis`: rot_dim / 2 ints or None."""
+    dt = FA_DTYPE[dtype] if isinstance(dtype, str) else int(dtype)
+    arr = None if strides is None else _strides_array(strides)
+    return int(load().fa_qk_norm_rope(q, k, q_out, k_out, q_weight, k_weight, positions, inv_freq,
+                                      int(B), int(S), int(H), int(H_kv), int(D), int(rot_dim),
+                                      int(n_axes), _axes_array(pair_axis), int(bool(interleaved)),
+                                      int(bool(norm)), float(eps), arr, dt, stream))
+
+
+def fa_qk_norm_rope_bwd_workspace_size(D):
+    """(status, bytes) of device workspace the weight gradients need."""
+    n = ctypes.c_size_t(0)
+    st = int(load().fa_qk_norm_rope_bwd_workspace_size(int(D), ctypes.byref(n)))
+    return st, int(n.value)
+
+
+def fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, q_weight, k_weight, dq_weight, dk_weight,
+                        positions, inv_freq, B, S, H, H_kv, D, rot_dim, n_axes, pair_axis,
+                        interleaved, norm, eps, strides, dtype, workspace, workspace_bytes,
+                        stream=None) -> int:
+    """Gradients of fa_qk_norm_rope: six stride triples for dq_out, dk_out, q, k, dq, dk."""
+    dt = FA_DTYPE[dtype] if isinstance(dtype, str) else int(dtype)
+    arr = None if strides is None else _strides_array(strides)
+    return int(load().fa_qk_norm_rope_bwd(dq_out, dk_out, q, k, dq, dk, q_weight, k_weight,
+                                          dq_weight, dk_weight, positions, inv_freq, int(B), int(S),
+                                          int(H), int(H_kv), int(D), int(rot_dim), int(n_axes),
+                                          _axes_array(pair_axis), int(bool(interleaved)),
+                                          int(bool(norm)), float(eps), arr, dt, workspace,
+                                          int(workspace_bytes), stream))
+
+
+def fa_kv4_write(k, v, slot_map, k_codes, k_scales, v_codes, v_scales, descale_k, descale_v,
+                 n_tokens, H_kv, D, page_size, num_pages, strides, dtype, stream=None) -> int:
+    """Rows of k and v into slots of the 4-bit cache: `strides` = two (batch, head, seq) triples."""
+    dt = FA_DTYPE[dtype] if isinstance(dtype, str) else int(dtype)
+    arr = None if strides is None else _strides_array(strides)
+    return int(load().fa_kv4_write(k, v, slot_map, k_codes, k_scales, v_codes, v_scales,
+                                   float(descale_k), float(descale_v), int(n_tokens), int(H_kv),
+                                   int(D), int(page_size), int(num_pages), arr, dt, stream))
+
+
+def fa_kv4_read(k_codes, k_scales, v_codes, v_scales, slot_map, k_out, v_out, descale_k, descale_v,
+                n_tokens, H_kv, D, page_size, num_pages, dtype, stream=None) -> int:
+    """Rows of the 4-bit cache back in 16 bits."""
+    dt = FA_DTYPE[dtype] if isinstance(dtype, str) else int(dtype)
+    return int(load().fa_kv4_read(k_codes, k_scales, v_codes, v_scales, slot_map, k_out, v_out,
+                                  float(descale_k), float(descale_v), int(n_tokens), int(H_kv),
+                                  int(D), int(page_size), int(num_pages), dt, stream))
+
+
+def fa_fwd_paged_kv4_workspace_size(n_seqs, max_seqlen_q, total_k, H, H_kv, D):
+    """(status, bytes) of device workspace fa_fwd_paged_kv4 needs."""
+    n = ctypes.c_size_t(0)
+    st = int(load().fa_fwd_paged_kv4_workspace_size(int(n_seqs), int(max_seqlen_q), int(total_k),
+                                                    int(H), int(H_kv), int(D), ctypes.byref(n)))
+    return st, int(n.value)
+
+
+def fa_fwd_paged_kv4(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_q, seqused_k, block_table,
+                     n_seqs, max_pages, page_size, num_pages, total_q, max_seqlen_q, total_k, H,
+                     H_kv, D, scale, causal, dtype, descale_k, descale_v, workspace,
+                     workspace_bytes, stream=None) -> int:
+    """Packed queries against the 4-bit paged cache (device pointers; causal 0 / 1 / 2)."""
+    dt = FA_DTYPE[dtype] if isinstance(dtype, str) else int(dtype)
+    c = CAUSAL[causal] if isinstance(causal, str) else int(causal)
+    return int(load().fa_fwd_paged_kv4(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_q,
+                                       seqused_k, block_table, int(n_seqs), int(max_pages),
+                                       int(page_size), int(num_pages), int(total_q),
+                                       int(max_seqlen_q), int(total_k), int(H), int(H_kv), int(D),
+                                       float(scale), c, dt, float(descale_k), float(descale_v),
+                                       workspace, int(workspace_bytes), stream))
 
 
 def fa_last_device_error(stream=None) -> int:
