@@ -438,7 +438,8 @@ fa_status_t fa_paged_slots(const int32_t* past_k, const int32_t* new_q, const in
  *   positions: int32 [n_axes, B, S], any value of the type; n_axes 1..4.
  *   inv_freq: double [rot_dim / 2], radians a position (a device array).
  *     The angle is reduced modulo a turn in 64-bit integers, so that it is as
- *     exact at position 2^31 as at 1; a frequency that is not finite reads as 0.
+ *     exact at position 2^31 as at 1; a frequency that is not finite, or 2^64 and more,
+ *     reads as 0.
  *   pair_axis: HOST array [rot_dim / 2] of axes, each < n_axes; NULL: all 0.
  *   rot_dim: 0 (norm only; positions and inv_freq may be NULL) or a multiple
  *     of 16 up to D.  norm = 0 with rot_dim = 0 is FA_ERR_INVALID_ARG.

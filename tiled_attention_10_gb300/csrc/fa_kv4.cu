@@ -26,6 +26,7 @@
 
 #include "../../include/fa_api.h"
 #include "fa_kv4.cuh"
+#include "fa_launch.cuh"
 
 namespace {
 
@@ -88,6 +89,7 @@ template <> __device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float a, flo
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const __grid_constant__ RowParams p) {
+  fa::wait_for_stream();
   const int which = blockIdx.y;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   if (i >= p.n_groups) return;
@@ -139,6 +141,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const __grid_con
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) fa_kv4_read_kernel(const __grid_constant__ RowParams p) {
+  fa::wait_for_stream();
   const int which = blockIdx.y;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   if (i >= p.n_groups) return;
@@ -208,11 +211,8 @@ RowParams params(const uint8_t* kc, const uint8_t* ks, const uint8_t* vc, const 
 
 template <typename K>
 fa_status_t launch(K kernel, const RowParams& p, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((p.n_groups + kThreads - 1) / kThreads), 2);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const fa::Launch c(dim3(static_cast<unsigned>((p.n_groups + kThreads - 1) / kThreads), 2), kThreads, 0, stream);
+  return cudaLaunchKernelEx(&c.cfg, kernel, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace

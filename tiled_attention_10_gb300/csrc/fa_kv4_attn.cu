@@ -46,6 +46,7 @@
 
 #include "../../include/fa_api.h"
 #include "fa_kv4.cuh"
+#include "fa_launch.cuh"
 
 namespace {
 
@@ -54,10 +55,11 @@ using fa::kv4::codes_to_half;
 using fa::kv4::mul_half;
 using fa::kv4::scales_to_half;
 
-constexpr int kWarps = 4;           // warps of a block
 constexpr int kStep = 32;           // keys of a warp's step
 constexpr int kChunk = 64;          // keys of a unit of work
-constexpr int kMinChunks = 4;       // least chunks worth a block of their own
+constexpr int kUnitCost = 8;        // chunks that a unit costs beside its own, for an even split
+constexpr int kMinShare = kUnitCost + 4;   // least work of a block, in chunks: any run longer than
+                                    // kUnitCost holds keys
 constexpr int kMaxSms = 160;
 constexpr float kBias = 8.0f;       // P is held as 2^(score - max + kBias): small
                                     // probabilities stay normal numbers of f16
@@ -112,11 +114,16 @@ __device__ __forceinline__ Seq sequence(const AttnParams& p, int s) {
   return q;
 }
 
-__device__ __forceinline__ int64_t chunks_of(const AttnParams& p, const Seq& q) {
-  return static_cast<int64_t>(p.cache.H_kv) * q.tiles * q.chunks;
+// A sequence's work, in chunks: its units' keys and their fixed costs.
+__device__ __forceinline__ int64_t work_of(const AttnParams& p, const Seq& q) {
+  return q.chunks > 0 ? static_cast<int64_t>(p.cache.H_kv) * q.tiles * (q.chunks + kUnitCost) : 0;
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes of which the first `bytes` come from src, zeros behind them.
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -163,208 +170,339 @@ __device__ __forceinline__ int v_place(int r, int c) {
   return ((r & ~7) | ((r & 1) << 2) | ((r >> 1) & 3)) * 32 + c * 16;
 }
 
-// The codes and scales of keys [key0, key0 + 32) into a ring stage; keys from
-// `end` on, and pages outside the cache, become zeros.
-template <int D>
-__device__ __forceinline__ void load_step(const AttnParams& p, uint32_t stage, int head, int key0, int end,
-                                          const int (&page)[2], int lane) {
-  using St = Stage<D>;
-  const int ps = p.cache.page_size;
-  int64_t row[2];
-  bool ok[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int key = key0 + 16 * h;
-    const int in_page = p.page_shift >= 0 ? key & (ps - 1) : key % ps;
-    ok[h] = page[h] >= 0 && page[h] < p.cache.num_pages;
-    row[h] = (static_cast<int64_t>(ok[h] ? page[h] : 0) * p.cache.H_kv + head) * ps + (ok[h] ? in_page : 0);
+// Where the next step's keys are: pages of its two halves (one lookup when
+// pages hold 32 keys or more) and the first key's row in its page.
+struct Place {
+  int page[2], in_page;
+};
+__device__ __forceinline__ Place look_up(const AttnParams& p, uint32_t table, int key0, int end) {
+  Place at = {{-1, -1}, 0};
+  if (key0 < end) {
+    const int ps = p.cache.page_size;
+    const int col = p.page_shift >= 0 ? key0 >> p.page_shift : key0 / ps;
+    at.in_page = key0 - col * ps;
+    at.page[0] = p.block_table[table + col];
+    at.page[1] = ps >= kStep ? at.page[0] : key0 + 16 < end ? p.block_table[table + col + 1] : -1;
   }
-  constexpr int C = St::kChunksRow, kPer = kStep * C / 32;   // pieces a lane, of K and of V
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int piece = lane + 32 * i, r = piece / C, c = piece % C;
-    const int h = i * 2 / kPer;                              // the half that row r is in
-    const int64_t at = (row[h] + (r & 15)) * (D / 2) + c * 16;
-    const bool in = ok[h] && key0 + r < end;
-    const int64_t from = in ? at : 0;
-    copy16(stage + r * (D / 2) + c * 16, p.cache.codes[0] + from, in ? 16 : 0);
-    copy16(stage + St::kV + v_place<D>(r, c), p.cache.codes[1] + from, in ? 16 : 0);
-  }
-  // scales: D / 16 bytes a key; 16-byte pieces hold 256 / D keys
-  constexpr int KP = 256 / D, N = kStep / KP;                // keys a piece, pieces
-  if (lane < 2 * N) {
-    const int which = lane / N, piece = lane % N, r = piece * KP, h = r >> 4;
-    const int keys = ok[h] ? min(max(end - key0 - r, 0), KP) : 0;
-    const int64_t at = keys > 0 ? (row[h] + (r & 15)) * (D / 16) : 0;
-    copy16(stage + (which ? St::kVs : St::kKs) + piece * 16, p.cache.scales[which] + at, keys * (D / 16));
-  }
+  return at;
 }
 
-__device__ __forceinline__ int page_index(const AttnParams& p, int key) {
-  return p.page_shift >= 0 ? key >> p.page_shift : key / p.cache.page_size;
-}
-__device__ __forceinline__ void look_up(const AttnParams& p, const int32_t* table, int key0, int end, int (&page)[2]) {
+// A lane's sources and destinations in a step's copies.
+struct Lane {
+  uint32_t v_dst, s_dst;     // offsets in a stage of its first piece of V and its piece of scales
+};
+
+// The codes and scales of keys [key0, key0 + 32) into a ring stage; keys from
+// `end` on, and pages outside the cache, become zeros.  Rows of a page are
+// one run of memory, so a lane's pieces lie 512 bytes apart.
+template <int D>
+__device__ __forceinline__ void load_step(const AttnParams& p, const Lane& me, uint32_t stage, int head, int key0,
+                                          int end, const Place& at, int lane) {
+  using St = Stage<D>;
+  constexpr int C = St::kChunksRow, kHalf = 16 * C / 32;     // pieces of K (or V) a lane takes of 16 keys
+  constexpr int KP = 256 / D, N = kStep / KP;                // keys a piece of scales holds, pieces
+  const uint32_t pages = static_cast<uint32_t>(p.cache.num_pages), ps = p.cache.page_size;
+  uint32_t row[2];
+  row[0] = (static_cast<uint32_t>(at.page[0]) * p.cache.H_kv + head) * ps + at.in_page;
+  row[1] = row[0] + 16;
+  if (ps < kStep) row[1] = (static_cast<uint32_t>(at.page[1]) * p.cache.H_kv + head) * ps;
+  const bool ok0 = static_cast<uint32_t>(at.page[0]) < pages, ok1 = static_cast<uint32_t>(at.page[1]) < pages;
+  if (ok0 && ok1 && key0 + kStep <= end) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint64_t off = static_cast<uint64_t>(row[h]) * (D / 2) + lane * 16;
+      const uint8_t *k = p.cache.codes[0] + off, *v = p.cache.codes[1] + off;
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) {
+        copy16(stage + lane * 16 + (h * kHalf + i) * 512, k + i * 512);
+        copy16(stage + me.v_dst + (h * kHalf + i) * 512, v + i * 512);
+      }
+    }
+    if (2 * N == 32 || lane < 2 * N) {
+      const int h = (lane % N) * KP / 16;
+      copy16(stage + me.s_dst, p.cache.scales[lane / N % 2] + static_cast<uint64_t>(row[h] + (lane % N) * KP - 16 * h) * (D / 16));
+    }
+    return;
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int key = key0 + 16 * h;
-    page[h] = key < end ? table[page_index(p, key)] : -1;
+    const bool ok = h ? ok1 : ok0;
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) {
+      const int r = (lane + 32 * i) / C;                     // row of the half
+      const bool in = ok && key0 + 16 * h + r < end;
+      const uint64_t off = in ? static_cast<uint64_t>(row[h]) * (D / 2) + i * 512 + lane * 16 : 0;
+      copy16_or_zero(stage + lane * 16 + (h * kHalf + i) * 512, p.cache.codes[0] + off, in ? 16 : 0);
+      copy16_or_zero(stage + me.v_dst + (h * kHalf + i) * 512, p.cache.codes[1] + off, in ? 16 : 0);
+    }
+  }
+  if (lane < 2 * N) {
+    const int r = (lane % N) * KP, h = r >> 4;
+    const int keys = (h ? ok1 : ok0) ? min(max(end - key0 - r, 0), KP) : 0;
+    const uint64_t off = keys > 0 ? static_cast<uint64_t>(row[h] + r - 16 * h) * (D / 16) : 0;
+    copy16_or_zero(stage + me.s_dst, p.cache.scales[lane / N % 2] + off, keys * (D / 16));
   }
 }
 
 template <int D, int NT>
 struct Cfg {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kBlocks = NT == 1 ? 4 : NT == 2 ? 3 : 2;   // resident blocks an SM
-  static constexpr int kStages = NT == 1 ? 3 : 4;
-  static constexpr int kRing = kStages * Stage<D>::kBytes;        // a warp's ring
-  // at the end of a run a warp's O takes the place of its ring
-  static constexpr int kWarpBytes = kRing > kRows * D * 4 ? kRing : kRows * D * 4;
-  static constexpr int kSmem = kWarps * kWarpBytes;
+  // Warps of a block and resident blocks an SM: 16 warps of 128 registers with
+  // 8 rows, 12 of 168 with 16, 8 of 255 with 32 (O and the ring grow).
+  static constexpr int kWarps = NT == 1 ? 8 : 4;
+  static constexpr int kBlocks = NT == 2 ? 3 : 2;
+  // A warp's ring: three stages; at the end of a unit its O lies in the third
+  // one's place (and behind it), while the next unit's first two steps are
+  // already on their way to the other two.
+  static constexpr int kStages = 3;
+  static constexpr int kOut = 2 * Stage<D>::kBytes;
+  static constexpr int kWarpBytes = kOut + (Stage<D>::kBytes > kRows * D * 4 ? Stage<D>::kBytes : kRows * D * 4);
+  static constexpr int kQ = kWarps * kWarpBytes;                  // the unit's Q, f16, in operand order
+  static constexpr int kSmem = kQ + kRows * D * 2;
 };
 
+// One unit of work: a run of chunks of one (sequence, head, row tile).
+struct Unit {
+  int64_t q_row0;                   // the sequence's first row of q
+  int32_t s, head, row0, rows;      // row0: first row (token * G + head) of the tile
+  int32_t key_begin, key_end;
+  int32_t keys, q_len, k_len;       // of the sequence, see Seq
+  int32_t piece;                    // -1: the whole (sequence, head, tile); else the partial's slot
+  int32_t pieces;                   // of a divided one that starts here, else 0
+  int32_t more;                     // another unit of this block follows
+};
+
+// Where a block is in its run of chunks (kept by its first thread).
+struct Cursor {
+  int64_t w, w1, off, total, blocks;   // next place, end; offset in the sequence; of the launch
+  int32_t s;
+  Seq sq;
+};
+
+// The cursor's next unit (moving on to the sequence that has it).
+template <int ROWS>
+__device__ __noinline__ void next_unit(const AttnParams& p, Cursor& c, Unit& u) {
+  int64_t all = work_of(p, c.sq);
+  while (c.off >= all) {
+    c.off -= all;
+    c.sq = sequence<ROWS>(p, ++c.s);
+    all = work_of(p, c.sq);
+  }
+  const Seq& sq = c.sq;
+  // A unit is kUnitCost places without keys and then its chunks; this block's
+  // run covers its places [pos, end).
+  const int size = sq.chunks + kUnitCost;
+  const int64_t unit = c.off / size;
+  const int pos = static_cast<int>(c.off - unit * size);
+  const int end = static_cast<int>(min(static_cast<int64_t>(size), pos + (c.w1 - c.w)));
+  const int c0 = max(pos - kUnitCost, 0), c1 = end - kUnitCost;
+  u.q_row0 = sq.q_row0;
+  u.s = c.s;
+  u.head = static_cast<int>(unit / sq.tiles);
+  u.row0 = static_cast<int>(unit - static_cast<int64_t>(u.head) * sq.tiles) * ROWS;
+  u.rows = static_cast<int>(min(static_cast<int64_t>(ROWS), static_cast<int64_t>(sq.q_len) * p.G - u.row0));
+  u.key_begin = c0 * kChunk;
+  u.key_end = min(c1 * kChunk, sq.k_len);
+  u.keys = sq.keys;
+  u.q_len = sq.q_len;
+  u.k_len = sq.k_len;
+  // a block's first unit may continue one, its last may be continued
+  u.piece = c0 > 0 ? 0 : c1 < sq.chunks ? 1 : -1;
+  u.pieces = 0;
+  if (u.piece == 1)   // up to the block that holds the unit's last chunk
+    u.pieces = static_cast<int32_t>(((c.w - pos + size) * c.blocks - 1) / c.total - blockIdx.x + 1);
+  c.w += end - pos;
+  c.off += end - pos;
+  u.more = c.w1 - c.w > kUnitCost;    // (what is left begins with a unit: has it keys?)
+}
+
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks)
+__global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, Cfg<D, NT>::kBlocks)
     fa_kv4_attn_kernel(const __grid_constant__ AttnParams p) {
   using C = Cfg<D, NT>;
   using St = Stage<D>;
-  constexpr int kRows = C::kRows;
+  constexpr int kRows = C::kRows, kWarps = C::kWarps;
   constexpr int MT = D / 16;        // 16-element tiles of O^T
-  constexpr int QW = D / 8;         // f16 pairs of Q a lane holds for a row
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float w_max[kWarps][kRows], w_sum[kWarps][kRows];
-  __shared__ int64_t scan[kWarps], start_off;
-  __shared__ int start_seq;
+  constexpr int QW = D / 8;         // f16 pairs of a row of Q in one lane's dimensions
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float w_max[kWarps][kRows], w_sum[kWarps][kRows], row_scale[kRows];
+  __shared__ int row_limit[kRows];
+  __shared__ int64_t scan[kWarps];
+  __shared__ Cursor cursor;
+  __shared__ Unit units[4];               // of a ring: this one, the next two
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
+  fa::wait_for_stream();
 
-  // ---- this block's run of chunks [w0, w1)
-  const int per = (p.n_seqs + kWarps * 32 - 1) / (kWarps * 32);
-  const int s0 = min(p.n_seqs, tid * per), s1 = min(p.n_seqs, s0 + per);
-  int64_t mine = 0;
-  for (int s = s0; s < s1; ++s) mine += chunks_of(p, sequence<kRows>(p, s));
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t a = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += a;
-  }
-  if (lane == 31) scan[warp] = incl;
-  __syncthreads();
-  int64_t before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-  }
-  const int64_t blocks = min(static_cast<int64_t>(gridDim.x), (total + kMinChunks - 1) / kMinChunks);
-  const int64_t bid = blockIdx.x;
-  if (tid == 0) p.meta[bid].pieces = 0;
-  if (bid >= blocks) return;
-  int64_t w = total * bid / blocks;
-  const int64_t w1 = total * (bid + 1) / blocks;
-  if (w >= before && w < before + mine) {
-    int64_t off = w - before;
-    int s = s0;
-    for (;; ++s) {
-      const int64_t c = chunks_of(p, sequence<kRows>(p, s));
-      if (off < c) break;
-      off -= c;
+  // ---- this block's run of the work and the sequence it starts in
+  {
+    const int per = (p.n_seqs + kWarps * 32 - 1) / (kWarps * 32);
+    const int s0 = min(p.n_seqs, tid * per), s1 = min(p.n_seqs, s0 + per);
+    int64_t mine = 0;
+    Seq sq = {};
+    for (int s = s0; s < s1; ++s) {
+      sq = sequence<kRows>(p, s);
+      mine += work_of(p, sq);
     }
-    start_seq = s;
-    start_off = off;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t a = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += a;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += scan[w];
+      total += scan[w];
+    }
+    const int64_t blocks = total == 0 ? 0 : min(static_cast<int64_t>(gridDim.x), max(total / kMinShare, int64_t(1)));
+    const int64_t bid = blockIdx.x;
+    if (tid == 0) p.meta[bid].pieces = 0;
+    if (bid >= blocks) return;
+    const int64_t w = total * bid / blocks;
+    if (w >= before && w < before + mine) {   // one thread has the sequence
+      int64_t off = w - before;
+      int s = s0;
+      if (per > 1) {                          // (else sq is the one sequence already)
+        for (;; ++s) {
+          sq = sequence<kRows>(p, s);
+          const int64_t c = work_of(p, sq);
+          if (off < c) break;
+          off -= c;
+        }
+      }
+      cursor = Cursor{w, total * (bid + 1) / blocks, off, total, blocks, s, sq};
+      next_unit<kRows>(p, cursor, units[0]);
+      if (units[0].more) next_unit<kRows>(p, cursor, units[1]);
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  int s = start_seq;
-  int64_t off = start_off;
 
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kWarpBytes;
   uint8_t* const ring_p = smem + warp * C::kWarpBytes;
-  float* const warp_o = reinterpret_cast<float*>(ring_p);
+  Lane me;
+  {
+    constexpr int CR = St::kChunksRow, KP = 256 / D, N = kStep / KP;
+    me.v_dst = St::kV + v_place<D>(lane / CR, lane % CR);
+    const int which = lane / N % 2, piece = lane % N;
+    me.s_dst = (which ? St::kVs : St::kKs) + piece * 16;
+  }
+  // this lane's reads of a stage, relative to it
+  const int k_at = D == 128 ? g * 64 + t * 16 : g * 32 + t * 8;
+  const int ks_at = St::kKs + (D == 128 ? g * 8 + t * 2 : g * 4 + t);
+  const int v0_at = St::kV + (D == 128 ? v_place<D>(2 * t, g >> 1) + (g & 1) * 8 : v_place<D>(2 * t, g >> 2) + (g & 3) * 4);
+  const int v1_at = v0_at + 128;            // v_place of row 2 t + 1 at both D
+  const int vs_at = St::kVs + (D == 128 ? t * 16 + g : t * 8 + (g >> 1));
+  uint8_t* const q_smem = smem + C::kQ;
+  const int step = kWarps * kStep;
 
-  while (w < w1) {
-    const Seq sq = sequence<kRows>(p, s);
-    const int64_t all = chunks_of(p, sq);
-    if (off >= all) {                       // an empty sequence, or this one is done
-      off -= all;
-      ++s;
-      continue;
-    }
-    const int64_t unit = off / sq.chunks;
-    const int c0 = static_cast<int>(off - unit * sq.chunks);
-    const int c1 = static_cast<int>(min(static_cast<int64_t>(sq.chunks), c0 + (w1 - w)));
-    const int head = static_cast<int>(unit / sq.tiles);
-    const int tile_row0 = static_cast<int>(unit - static_cast<int64_t>(head) * sq.tiles) * kRows;
-    const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(sq.q_len) * p.G - tile_row0));
-    const int key_begin = c0 * kChunk, key_end = min(c1 * kChunk, sq.k_len);
-    const int32_t* table = p.block_table + static_cast<int64_t>(s) * p.max_pages;
-
-    // ---- start the ring
-    const int step = kWarps * kStep;
-    int next = key_begin + warp * kStep;     // first key of the next step to load
-    int page[2];
-    look_up(p, table, next, key_end, page);
+  Place at;                                 // of the next step to load
+  uint32_t table;                           // the sequence's row of the block table
+  auto start_ring = [&](const Unit& u) {
+    const int end = u.key_end;
+    table = static_cast<uint32_t>(u.s) * static_cast<uint32_t>(p.max_pages);
+    int next = u.key_begin + warp * kStep;
+    at = look_up(p, table, next, end);
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) {
-      if (next < key_end) load_step<D>(p, ring + i * St::kBytes, head, next, key_end, page, lane);
+      if (next < end) load_step<D>(p, me, ring + i * St::kBytes, u.head, next, end, at, lane);
       copies_commit();
       next += step;
-      look_up(p, table, next, key_end, page);
+      at = look_up(p, table, next, end);
     }
+  };
 
-    // ---- Q: this lane's dimensions of row 8 j + g, and the rows' scales
-    uint32_t q[NT][QW];
-    float sl2[NT][2];
-    int limit[NT][2];                       // keys that the lane's two rows see
+  // Q: warp j takes rows 8 j .. 8 j + 7 of a unit; lane (g, t) its dimensions of
+  // row 8 j + g.  Loaded before the last unit's rows are joined, turned into
+  // operands after that.
+  constexpr int kQTiles = (NT + kWarps - 1) / kWarps;
+  uint4 q_raw[kQTiles][QW / 4];
+  auto load_q = [&](const Unit& u) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int r = 8 * j + g;
-      float rescale = 1.0f;
-      const int row = tile_row0 + r;
-      const int tok = row / p.G;
-      if (r < rows) {
-        const int64_t at = ((sq.q_row0 + tok) * p.H + static_cast<int64_t>(head) * p.G + (row - tok * p.G)) * D + t * (D / 4);
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at);
+    for (int i = 0; i < kQTiles; ++i) {
+      const int r = 8 * (warp + i * kWarps) + g, row = u.row0 + r, tok = row / p.G;
 #pragma unroll
-        for (int i = 0; i < QW / 4; ++i) {
-          const uint4 v = src[i];
-          q[j][4 * i] = v.x; q[j][4 * i + 1] = v.y; q[j][4 * i + 2] = v.z; q[j][4 * i + 3] = v.w;
-        }
-      } else {
+      for (int x = 0; x < QW / 4; ++x) q_raw[i][x] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < u.rows) {
+        const int64_t from = ((u.q_row0 + tok) * p.H + static_cast<int64_t>(u.head) * p.G + (row - tok * p.G)) * D + t * (D / 4);
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + from);
 #pragma unroll
-        for (int i = 0; i < QW; ++i) q[j][i] = 0u;
+        for (int x = 0; x < QW / 4; ++x) q_raw[i][x] = src[x];
       }
+    }
+  };
+  auto turn_q = [&](const Unit& u) {
+#pragma unroll
+    for (int i = 0; i < kQTiles; ++i) {
+      const int j = warp + i * kWarps;
+      if (j >= NT) break;                   // the same for the whole warp
+      uint32_t q[QW];
+#pragma unroll
+      for (int x = 0; x < QW / 4; ++x) {
+        q[4 * x] = q_raw[i][x].x; q[4 * x + 1] = q_raw[i][x].y; q[4 * x + 2] = q_raw[i][x].z; q[4 * x + 3] = q_raw[i][x].w;
+      }
+      float rescale = 1.0f;
       if (!std::is_same<T, __half>::value) {
         // bf16: shift the row by a power of two so that its largest value is
         // in [2^8, 2^9) and convert: exact down to 2^-22 of the largest.
         uint32_t top = 0u;
 #pragma unroll
-        for (int i = 0; i < QW; ++i) top = max(top, max(q[j][i] & 0x7fffu, (q[j][i] >> 16) & 0x7fffu));
+        for (int x = 0; x < QW; ++x) top = max(top, max(q[x] & 0x7fffu, (q[x] >> 16) & 0x7fffu));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = min(max(static_cast<int>(top >> 7), 30), 254);   // biased exponent
         const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 + 127 - e) << 23);
         rescale = __uint_as_float(static_cast<uint32_t>(e - 8) << 23);
 #pragma unroll
-        for (int i = 0; i < QW; ++i)
-          q[j][i] = pack_half(__uint_as_float(q[j][i] << 16) * up, __uint_as_float(q[j][i] & 0xffff0000u) * up);
+        for (int x = 0; x < QW; ++x)
+          q[x] = pack_half(__uint_as_float(q[x] << 16) * up, __uint_as_float(q[x] & 0xffff0000u) * up);
       }
       if (p.negate) {
 #pragma unroll
-        for (int i = 0; i < QW; ++i) q[j][i] ^= 0x80008000u;
+        for (int x = 0; x < QW; ++x) q[x] ^= 0x80008000u;
       }
-      int see = sq.k_len;
-      if (p.causal == FA_CAUSAL_TOP_LEFT) see = min(see, tok + 1);
-      if (p.causal == FA_CAUSAL_BOTTOM_RIGHT) see = min(see, tok + 1 + sq.keys - sq.q_len);
-      // the accumulators of this lane are rows 8 j + 2 t and 8 j + 2 t + 1
+      // [8 dimensions of a lane][lane]: 16 bytes, the two k16 steps of a word of codes
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        sl2[j][c] = fmaxf(p.sl2 * __shfl_sync(0xffffffffu, rescale, (2 * t + c) * 4), 1e-30f);
-        limit[j][c] = __shfl_sync(0xffffffffu, see, (2 * t + c) * 4);
+      for (int x = 0; x < QW / 4; ++x)
+        *reinterpret_cast<uint4*>(q_smem + ((j * (QW / 4) + x) * 32 + lane) * 16) =
+            make_uint4(q[4 * x], q[4 * x + 1], q[4 * x + 2], q[4 * x + 3]);
+      const int r = 8 * j + g, tok = (u.row0 + r) / p.G;
+      int see = u.k_len;
+      if (p.causal == FA_CAUSAL_TOP_LEFT) see = min(see, tok + 1);
+      if (p.causal == FA_CAUSAL_BOTTOM_RIGHT) see = min(see, tok + 1 + u.keys - u.q_len);
+      if (t == 0) {
+        row_scale[r] = fmaxf(p.sl2 * rescale, 1e-30f);
+        row_limit[r] = see;
       }
     }
-    int full = limit[0][0];                  // keys that all rows of the tile see
+  };
+
+  start_ring(units[0]);
+  load_q(units[0]);
+  turn_q(units[0]);
+  __syncthreads();
+  for (int turn = 0;; turn = (turn + 1) & 3) {
+    const Unit& un = units[turn];
+    int key_begin = un.key_begin, key_end = un.key_end, head = un.head;
+    // kept in registers: not to be read from shared memory again at every step
+    asm volatile("" : "+r"(key_begin), "+r"(key_end), "+r"(head));
+    // one warp looks for the unit after the next (known to all at the next one)
+    if (lane == 0 && warp == (turn & (kWarps - 1)) && un.more && units[(turn + 1) & 3].more)
+      next_unit<kRows>(p, cursor, units[(turn + 2) & 3]);
+    __syncwarp();
+    // this lane's accumulators are rows 8 j + 2 t and 8 j + 2 t + 1
+    float sl2[NT][2];
+    int full = key_end;                      // keys that all rows see
 #pragma unroll
-    for (int j = 0; j < NT; ++j) full = min(full, min(limit[j][0], limit[j][1]));
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        sl2[j][c] = row_scale[8 * j + 2 * t + c];
+        full = min(full, row_limit[8 * j + 2 * t + c]);
+      }
     full = min(full, __shfl_xor_sync(0xffffffffu, full, 1));
     full = min(full, __shfl_xor_sync(0xffffffffu, full, 2));
 
@@ -383,12 +521,30 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks)
       copies_wait<C::kStages - 2>();
       __syncwarp();
       const uint8_t* const st = ring_p + slot * St::kBytes;
+      // Shared memory is read well ahead of use, in the order written here (the
+      // votes and copies below keep the compiler from moving reads over them).
+      uint32_t words[2][2][D / 32], k_scale[2][2];   // [16 keys][8 keys]
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 16 * u + 8 * h;
+          if (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(st + k_at + r * 64);
+            words[u][h][0] = v.x; words[u][h][1] = v.y; words[u][h][2 % (D / 32)] = v.z; words[u][h][3 % (D / 32)] = v.w;
+            k_scale[u][h] = *reinterpret_cast<const uint16_t*>(st + ks_at + r * 8);
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(st + k_at + r * 32);
+            words[u][h][0] = v.x; words[u][h][1] = v.y;
+            k_scale[u][h] = st[ks_at + r * 4] * 0x101u;
+          }
+        }
       {
         const int into = slot == 0 ? C::kStages - 1 : slot - 1;   // the stage read one step ago
-        if (next < key_end) load_step<D>(p, ring + into * St::kBytes, head, next, key_end, page, lane);
+        const int next = key0 + (C::kStages - 1) * step;
+        if (next < key_end) load_step<D>(p, me, ring + into * St::kBytes, head, next, key_end, at, lane);
         copies_commit();
-        next += step;
-        look_up(p, table, next, key_end, page);
+        at = look_up(p, table, next + step, key_end);
       }
 
       // S^T: two tiles of 16 keys
@@ -397,53 +553,64 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks)
       for (int u = 0; u < 2; ++u) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) sc[u][j][0] = sc[u][j][1] = sc[u][j][2] = sc[u][j][3] = 0.0f;
-        uint32_t words[2][D / 32], s2[2][2];
+        uint32_t s2[2][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int r = 16 * u + 8 * h + g;
-          if (D == 128) {
-            const uint4 v = *reinterpret_cast<const uint4*>(st + r * 64 + t * 16);
-            words[h][0] = v.x; words[h][1] = v.y; words[h][2 % (D / 32)] = v.z; words[h][3 % (D / 32)] = v.w;
-            const uint32_t two = scales_to_half(*reinterpret_cast<const uint16_t*>(st + St::kKs + r * 8 + t * 2));
-            s2[h][0] = __byte_perm(two, 0u, 0x1010);
-            s2[h][1] = __byte_perm(two, 0u, 0x3232);
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(st + r * 32 + t * 8);
-            words[h][0] = v.x; words[h][1] = v.y;
-            const uint32_t b = st[St::kKs + r * 4 + t];
-            s2[h][0] = s2[h][1] = scales_to_half(b | (b << 8));
-          }
+          const uint32_t two = scales_to_half(k_scale[u][h]);
+          s2[h][0] = __byte_perm(two, 0u, 0x1010);
+          s2[h][1] = __byte_perm(two, 0u, 0x3232);
         }
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {          // a word: 8 dimensions, two k16 steps
           uint32_t a[2][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            codes_to_half(words[h][i], a[h]);
+            codes_to_half(words[u][h][i], a[h]);
 #pragma unroll
             for (int x = 0; x < 4; ++x) a[h][x] = mul_half(a[h][x], s2[h][i / 2]);
           }
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-              mma(sc[u][j], a[0][2 * x], a[1][2 * x], a[0][2 * x + 1], a[1][2 * x + 1], q[j][4 * i + 2 * x], q[j][4 * i + 2 * x + 1]);
+          for (int j = 0; j < NT; ++j) {
+            const uint4 b = *reinterpret_cast<const uint4*>(q_smem + ((j * (QW / 4) + i) * 32 + lane) * 16);
+            mma(sc[u][j], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+            mma(sc[u][j], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
+          }
         }
       }
+      // V of 16 keys: this lane's elements of keys 2 t, 2 t + 1 of each 8
+      constexpr int VW = D / 64;                     // words of a lane's elements of one key
+      uint32_t vx[2][2][VW], vy[2][2][VW], v_scale[2][2];
+      auto load_v = [&](int u) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 16 * u + 8 * h;
+          if (D == 128) {
+            const uint2 a = *reinterpret_cast<const uint2*>(st + v0_at + r * 64);
+            const uint2 b = *reinterpret_cast<const uint2*>(st + v1_at + r * 64);
+            vx[u][h][0] = a.x; vx[u][h][VW - 1] = a.y; vy[u][h][0] = b.x; vy[u][h][VW - 1] = b.y;
+            v_scale[u][h] = st[vs_at + r * 8] | (st[vs_at + r * 8 + 8] << 8);
+          } else {
+            vx[u][h][0] = *reinterpret_cast<const uint32_t*>(st + v0_at + r * 32);
+            vy[u][h][0] = *reinterpret_cast<const uint32_t*>(st + v1_at + r * 32);
+            v_scale[u][h] = st[vs_at + r * 4] | (st[vs_at + r * 4 + 4] << 8);
+          }
+        }
+      };
+      load_v(0);
 
       // softmax of the step, P to operands
-      const bool edge = key0 + kStep > min(full, key_end);
+      const bool edge = key0 + kStep > full;
       uint32_t pb[NT][4];                            // 8 keys each
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         if (edge) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+          for (int c = 0; c < 2; ++c) {
+            const int limit = min(row_limit[8 * j + 2 * t + c], key_end) - key0 - g;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int key = key0 + 16 * u + 8 * (x >> 1) + g;
-              if (key >= limit[j][x & 1] || key >= key_end) sc[u][j][x] = -CUDART_INF_F;
-            }
+            for (int x = 0; x < 4; ++x)
+              if (8 * x >= limit) sc[x >> 1][j][c + 2 * (x & 1)] = -CUDART_INF_F;
+          }
         }
         bool over = false;
         float top[2];
@@ -483,44 +650,22 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks)
       }
 
       // O^T += V^T P^T
+      load_v(1);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        constexpr int VW = D / 64;                   // words of a lane's elements of one key
-        uint32_t lo[2][VW], hi[2][VW], s2[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = 16 * u + 8 * h + 2 * t;
-          uint32_t x[VW], y[VW], sx, sy;
-          if (D == 128) {
-            const uint2 a = *reinterpret_cast<const uint2*>(st + St::kV + v_place<D>(r, g >> 1) + (g & 1) * 8);
-            const uint2 b = *reinterpret_cast<const uint2*>(st + St::kV + v_place<D>(r + 1, g >> 1) + (g & 1) * 8);
-            x[0] = a.x; x[VW - 1] = a.y; y[0] = b.x; y[VW - 1] = b.y;
-            sx = st[St::kVs + r * 8 + g];
-            sy = st[St::kVs + r * 8 + 8 + g];
-          } else {
-            x[0] = *reinterpret_cast<const uint32_t*>(st + St::kV + v_place<D>(r, g >> 2) + (g & 3) * 4);
-            y[0] = *reinterpret_cast<const uint32_t*>(st + St::kV + v_place<D>(r + 1, g >> 2) + (g & 3) * 4);
-            sx = st[St::kVs + r * 4 + (g >> 1)];
-            sy = st[St::kVs + r * 4 + 4 + (g >> 1)];
-          }
-          s2[h] = scales_to_half(sx | (sy << 8));
-#pragma unroll
-          for (int i = 0; i < VW; ++i) {             // bytes of two keys' codes of one element
-            lo[h][i] = (x[i] & 0x0f0f0f0fu) | ((y[i] << 4) & 0xf0f0f0f0u);
-            hi[h][i] = ((x[i] >> 4) & 0x0f0f0f0fu) | (y[i] & 0xf0f0f0f0u);
-          }
-        }
+        const uint32_t s2[2] = {scales_to_half(v_scale[u][0]), scales_to_half(v_scale[u][1])};
 #pragma unroll
         for (int i = 0; i < VW; ++i) {
           uint32_t a[2][2][4];                       // [key half][even / odd element][tile]
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            codes_to_half(lo[h][i], a[h][0]);
-            codes_to_half(hi[h][i], a[h][1]);
+          for (int h = 0; h < 2; ++h) {              // bytes of two keys' codes of one element
+            const uint32_t x = vx[u][h][i], y = vy[u][h][i];
+            codes_to_half((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), a[h][0]);
+            codes_to_half(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), a[h][1]);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
-              for (int x = 0; x < 4; ++x) a[h][e][x] = mul_half(a[h][e][x], s2[h]);
+              for (int x4 = 0; x4 < 4; ++x4) a[h][e][x4] = mul_half(a[h][e][x4], s2[h]);
           }
 #pragma unroll
           for (int x = 0; x < 4; ++x)
@@ -532,9 +677,12 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks)
       slot = slot == C::kStages - 1 ? 0 : slot + 1;
     }
 
+    // ---- the next unit's first keys start their way while this one ends
+    const bool more = un.more;
+    __syncwarp();                           // all lanes have read the ring's stages
+    if (more) start_ring(units[(turn + 1) & 3]);
+
     // ---- join the warps: rows of O in shared memory, then one sum a row
-    copies_wait<0>();
-    __syncwarp();
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -546,16 +694,14 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks)
         const int r = 8 * j + 2 * t + c;
         if (g == 0) { w_max[warp][r] = m[j][c]; w_sum[warp][r] = v; }
         // elements 16 g + 2 i + {0, 1} (D = 64: 8 g + ...)
-        float* dst = warp_o + r * D + g * (D / 8);
+        float* dst = reinterpret_cast<float*>(ring_p + C::kOut) + r * D + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
           *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(o[j][i][c], o[j][i][c + 2]);
       }
     __syncthreads();
-    const bool whole = c0 == 0 && c1 == sq.chunks;
-    const int piece = c0 == 0 ? 1 : 0;               // a block's first unit may continue
-                                                     // one, its last may be continued
-    for (int i = tid; i < rows * (D / 2); i += kWarps * 32) {
+    if (more) load_q(units[(turn + 1) & 3]);
+    for (int i = tid; i < un.rows * (D / 2); i += kWarps * 32) {
       const int r = i / (D / 2), d = (i % (D / 2)) * 2;
       float top = -CUDART_INF_F;
 #pragma unroll
@@ -564,7 +710,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks)
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
         const float a = w_max[k][r] == -CUDART_INF_F ? 0.0f : exp2f(w_max[k][r] - top);
-        const float2 v = *reinterpret_cast<const float2*>(smem + k * C::kWarpBytes + (r * D + d) * 4);
+        const float2 v = *reinterpret_cast<const float2*>(smem + k * C::kWarpBytes + C::kOut + (r * D + d) * 4);
         sum += a * w_sum[k][r];
         x += a * v.x;
         y += a * v.y;
@@ -572,85 +718,103 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, NT>::kBlocks)
       const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);   // NaN stays
       const float lse = sum == 0.0f ? -CUDART_INF_F
                                     : (top - kBias + log2f(sum)) * 0.69314718055994530942f;
-      if (whole) {
-        const int row = tile_row0 + r, tok = row / p.G, h = head * p.G + (row - tok * p.G);
-        const int64_t at = (sq.q_row0 + tok) * p.H + h;
+      if (un.piece < 0) {
+        const int row = un.row0 + r, tok = row / p.G, h = head * p.G + (row - tok * p.G);
+        const int64_t to = (un.q_row0 + tok) * p.H + h;
         const float dv = p.cache.descale[1] * inv;
-        T* dst = static_cast<T*>(p.o) + at * D + d;
+        T* dst = static_cast<T*>(p.o) + to * D + d;
         if (std::is_same<T, __half>::value)
           *reinterpret_cast<__half2*>(dst) = __floats2half2_rn(x * dv, y * dv);
         else
           *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(x * dv, y * dv);
-        if (d == 0) p.lse[static_cast<int64_t>(h) * p.total_q + sq.q_row0 + tok] = lse;
+        if (d == 0) p.lse[static_cast<int64_t>(h) * p.total_q + un.q_row0 + tok] = lse;
       } else {
-        const int64_t at = (bid * 2 + piece) * kRows + r;
-        *reinterpret_cast<float2*>(p.part_o + at * D + d) = make_float2(x * inv, y * inv);
-        if (d == 0) p.part_lse[at] = lse;
+        const int64_t to = (blockIdx.x * int64_t(2) + un.piece) * kRows + r;
+        *reinterpret_cast<float2*>(p.part_o + to * D + d) = make_float2(x * inv, y * inv);
+        if (d == 0) p.part_lse[to] = lse;
       }
     }
-    if (tid == 0 && c0 == 0 && !whole) {
-      // the block that holds the unit's last chunk
-      const int64_t last = w + sq.chunks - 1;
-      Meta& mt = p.meta[bid];
-      mt.q_row0 = sq.q_row0;
-      mt.head0 = head * p.G;
-      mt.row0 = tile_row0;
-      mt.rows = rows;
-      mt.pieces = static_cast<int32_t>(((last + 1) * blocks - 1) / total - bid + 1);
-    }
-    __syncthreads();                                  // the rings may be filled again
-    w += c1 - c0;
-    off += c1 - c0;
+    if (tid == 0 && un.pieces > 0)
+      p.meta[blockIdx.x] = Meta{un.q_row0, un.pieces, head * p.G, un.row0, un.rows};
+    if (!more) break;
+    turn_q(units[(turn + 1) & 3]);
+    __syncthreads();                        // O has been read, Q is written
   }
 }
 
-// Merge of a divided unit's pieces, one block a row:
+// Merge of a divided unit's pieces:
 //   lse = log sum exp(lse_i),  O = sum exp(lse_i - lse) O_i.
 // The first piece is the starting block's second slot, the others the
-// following blocks' first slots.
+// following blocks' first slots.  One block a unit; its warps share the rows,
+// several on one row where there are few, each over every n-th piece.
+constexpr int kMergeWarps = 16;
+
 template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(4 * D) fa_kv4_merge_kernel(const __grid_constant__ AttnParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__global__ void __launch_bounds__(kMergeWarps * 32) fa_kv4_merge_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int E = D / 32;              // elements a lane
+  __shared__ float sum_o[kMergeWarps][D], sum_w[kMergeWarps];
+  fa::wait_for_stream();
   const Meta mt = p.meta[blockIdx.x];
-  const int r = blockIdx.y;
-  if (mt.pieces == 0 || r >= mt.rows) return;
-  __shared__ float sum_o[4][D], sum_w[4];
-  const int d = threadIdx.x % D, part = threadIdx.x / D;
+  if (mt.pieces == 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int share = 1;                         // warps a row
+  while (2 * share * mt.rows <= kMergeWarps && share < 8) share *= 2;
   const int64_t first = blockIdx.x;
-  auto at = [&](int i) { return ((first + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + r; };
-  __shared__ float tops[4 * D / 32];
-  float top = -CUDART_INF_F;
-  for (int i = threadIdx.x; i < mt.pieces; i += 4 * D) top = fmaxf(top, p.part_lse[at(i)]);
+  for (int base = 0; base < mt.rows; base += kMergeWarps / share) {
+    const int r = base + warp / share, part = warp % share;
+    const bool in = r < mt.rows;
+    auto at = [&](int i) { return ((first + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + r; };
+    float top = -CUDART_INF_F, sum = 0.0f, acc[E];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = top;
-  __syncthreads();
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    if (in) {
+      for (int i = lane; i < mt.pieces; i += 32) top = fmaxf(top, p.part_lse[at(i)]);
 #pragma unroll
-  for (int i = 0; i < 4 * D / 32; ++i) top = fmaxf(top, tops[i]);
-  float acc = 0.0f, sum = 0.0f;
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll 4
-  for (int i = part; i < mt.pieces; i += 4) {
-    const int64_t a = at(i);
-    const float lse = p.part_lse[a];
-    const float wgt = lse == -CUDART_INF_F ? 0.0f : expf(lse - top);
-    sum += wgt;
-    acc += wgt * p.part_o[a * D + d];
+      for (int i = part; i < mt.pieces; i += share) {
+        const int64_t a = at(i);
+        const float lse = p.part_lse[a];
+        const float wgt = lse == -CUDART_INF_F ? 0.0f : expf(lse - top);
+        const float* src = p.part_o + a * D + lane * E;
+        sum += wgt;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += wgt * src[e];
+      }
+    }
+    if (share > 1) {                     // the row's warps, in order
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum_o[warp][lane * E + e] = acc[e];
+      if (lane == 0) sum_w[warp] = sum;
+      __syncthreads();
+      if (part == 0 && in) {
+        for (int k = 1; k < share; ++k) {
+          sum += sum_w[warp + k];
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += sum_o[warp + k][lane * E + e];
+        }
+      }
+    }
+    if (in && part == 0) {
+      const int row = mt.row0 + r, tok = row / p.G, h = mt.head0 + (row - tok * p.G);
+      const float mul = sum == 0.0f ? 0.0f : p.cache.descale[1] / sum;
+      uint16_t* dst = static_cast<uint16_t*>(p.o) + ((mt.q_row0 + tok) * p.H + h) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        uint32_t w;
+        if (std::is_same<T, __half>::value) {
+          w = pack_half(acc[e] * mul, acc[e + 1] * mul);
+        } else {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(acc[e] * mul, acc[e + 1] * mul);
+          w = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint32_t*>(dst + e) = w;
+      }
+      if (lane == 0)
+        p.lse[static_cast<int64_t>(h) * p.total_q + mt.q_row0 + tok] = sum == 0.0f ? -CUDART_INF_F : top + logf(sum);
+    }
+    // (share > 1 only where one pass takes all rows: the buffers are not reused)
   }
-  sum_o[part][d] = acc;
-  if (d == 0) sum_w[part] = sum;
-  __syncthreads();
-  if (part != 0) return;
-  acc = (sum_o[0][d] + sum_o[1][d]) + (sum_o[2][d] + sum_o[3][d]);
-  sum = (sum_w[0] + sum_w[1]) + (sum_w[2] + sum_w[3]);
-  const int row = mt.row0 + r, tok = row / p.G, h = mt.head0 + (row - tok * p.G);
-  const float v = sum == 0.0f ? 0.0f : acc / sum * p.cache.descale[1];
-  T* dst = static_cast<T*>(p.o) + ((mt.q_row0 + tok) * p.H + h) * D + d;
-  if (std::is_same<T, __half>::value)
-    *reinterpret_cast<__half*>(dst) = __float2half_rn(v);
-  else
-    *reinterpret_cast<__nv_bfloat16*>(dst) = __float2bfloat16_rn(v);
-  if (d == 0)
-    p.lse[static_cast<int64_t>(h) * p.total_q + mt.q_row0 + tok] = sum == 0.0f ? -CUDART_INF_F : top + logf(sum);
 }
 
 // ---------------------------------------------------------------- unpacking
@@ -674,6 +838,7 @@ __global__ void __launch_bounds__(kUnpackThreads) fa_kv4_unpack_kernel(const __g
   __shared__ int64_t warp_sum[kUnpackThreads / 32];
   __shared__ int64_t where[kUnpackRows];  // row (page, 0, row of the page) in the cache, or -1
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.n_seqs;
+  fa::wait_for_stream();
   // keys of a sequence: none where it brings no queries
   auto keys = [&](int s) -> int64_t {
     return p.cu_q[s + 1] > p.cu_q[s] ? min(max(static_cast<int64_t>(p.seqused_k[s]), int64_t(0)), p.max_keys) : 0;
@@ -788,7 +953,7 @@ struct Layout {
   size_t part_o, part_lse, meta, bytes;
 };
 Layout stream_layout(int64_t D, int nt) {
-  const size_t blocks = static_cast<size_t>(kMaxSms) * (nt == 1 ? 4 : nt == 2 ? 3 : 2);
+  const size_t blocks = static_cast<size_t>(kMaxSms) * (nt == 2 ? 3 : 2);     // Cfg::kBlocks
   Layout l;
   l.part_o = 0;
   l.part_lse = round256(blocks * 2 * 8 * nt * D * 4);
@@ -813,23 +978,12 @@ cudaError_t launch_stream(const AttnParams& p, int sms, cudaStream_t stream) {
   using C = Cfg<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(fa_kv4_attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(sms * C::kBlocks));
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = stream;
-  e = cudaLaunchKernelEx(&cfg, fa_kv4_attn_kernel<T, D, NT>, p);
+  const dim3 grid(static_cast<unsigned>(sms * C::kBlocks));
+  const fa::Launch c(grid, C::kWarps * 32, C::kSmem, stream);
+  e = cudaLaunchKernelEx(&c.cfg, fa_kv4_attn_kernel<T, D, NT>, p);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t mc = {};
-  mc.gridDim = dim3(static_cast<unsigned>(sms * C::kBlocks), C::kRows);
-  mc.blockDim = dim3(4 * D);
-  mc.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  mc.attrs = attr;
-  mc.numAttrs = 1;
-  return cudaLaunchKernelEx(&mc, fa_kv4_merge_kernel<T, D, C::kRows>, p);
+  const fa::Launch mc(grid, kMergeWarps * 32, 0, stream);
+  return cudaLaunchKernelEx(&mc.cfg, fa_kv4_merge_kernel<T, D, C::kRows>, p);
 }
 
 template <typename T, int D>
@@ -847,13 +1001,9 @@ cudaError_t launch_unpack(const UnpackParams& p, int sms, cudaStream_t stream) {
                                                static_cast<int>((kMaxUnpackSeqs + 1) * 4));
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg = {};
   const int64_t want = std::max<int64_t>(1, (p.total_k + kUnpackRows - 1) / kUnpackRows);
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(want, sms * 4)), 2);
-  cfg.blockDim = dim3(kUnpackThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, fa_kv4_unpack_kernel<T, D>, p);
+  const fa::Launch c(dim3(static_cast<unsigned>(std::min<int64_t>(want, sms * 4)), 2), kUnpackThreads, smem, stream);
+  return cudaLaunchKernelEx(&c.cfg, fa_kv4_unpack_kernel<T, D>, p);
 }
 
 }  // namespace
@@ -914,6 +1064,9 @@ fa_status_t fa_fwd_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_
   if (off(workspace, 256)) return FA_ERR_MISALIGNED;
   const int64_t G = H / H_kv, rows = max_seqlen_q * G;
   if (rows > kStreamRows && n_seqs > kMaxUnpackSeqs) return FA_ERR_UNSUPPORTED;
+  // a row's index in the cache is a 32-bit number (2^32 rows of D = 64, K and V, take 309 GB)
+  if (num_pages > static_cast<int64_t>(0xffffffffu) / (page_size * H_kv)) return FA_ERR_UNSUPPORTED;
+  if (n_seqs > static_cast<int64_t>(0xffffffffu) / max_pages_per_seq) return FA_ERR_UNSUPPORTED;
   if (total_q == 0) return FA_OK;
 
   const int sms = sm_count();

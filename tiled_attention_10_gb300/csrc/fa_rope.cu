@@ -4,19 +4,19 @@
  * over the data.
  *
  * Bound by HBM: 8 or so operations a value against 4 bytes moved (forward; 6
- * backward).  So one read and one write of each value, 16 bytes a lane, and
- * several rows in flight a lane:
- *   - a head vector lies in D / 8 lanes (16 at D = 128, 8 at 64), 8 values a
- *     lane, so sums over a head are 3 or 4 shuffles;
- *   - a warp takes one token and walks its heads, so the token's cosines and
- *     sines are worked out once (two pairs a lane, exchanged through shared
- *     memory) and stay in registers over all heads;
- *   - with few tokens the heads of one are cut into parts for several warps.
- * A value's partner in its rotation pair is in the same lane (interleaved) or
- * rot_dim / 16 lanes away (one shuffle).
+ * backward).  So one read and one write of each value, with the next rows'
+ * loads always in flight:
+ *   - a head vector lies in D / 8 lanes (16 at D = 128, 8 at 64), so sums over
+ *     a head are 4 or 3 shuffles; a lane holds both values of its rotation
+ *     pairs (four elements of the first half and their partners of the second,
+ *     two 8-byte accesses), so the rotation needs none;
+ *   - one block works out the cosines and sines of its one to four tokens, a
+ *     pair a thread, in shared memory; then each warp walks heads of one token
+ *     with that token's values and the weights in registers;
+ *   - with few tokens more warps share one.
  * The angle: a position times the frequency, in turns modulo 1, as a 64-bit
  * fixed-point product (wrapping is the reduction), so no position is too far
- * for 32-bit sine and cosine.
+ * for 32-bit sine and cosine; in integers, as this GPU has few fp64 units.
  */
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -28,12 +28,14 @@
 #include <cstring>
 
 #include "../../include/fa_api.h"
+#include "fa_launch.cuh"
 
 namespace {
 
 constexpr int kWarps = 8;
 constexpr int kMaxPairs = 64;
-constexpr int kBwdBlocks = 152 * 2;   // rows of the weight gradients' partial sums
+constexpr int kBwdResident = 2;       // blocks of the backward an SM holds
+constexpr int kBwdBlocks = 152 * kBwdResident;   // its grid: rows of the weight gradients' partial sums
 
 struct RopeParams {
   const void* x[2];        // q, k: the forward's inputs
@@ -46,49 +48,66 @@ struct RopeParams {
   float* partial;          // backward: [blocks, 2, D] weight gradient partials, or null
   int64_t B, S;
   int32_t heads[2];
-  int32_t parts;           // warps that share a token's heads
+  int32_t share;           // warps that share a token: 1, 2, 4 or 8
   int32_t rot;             // rotated elements
   float eps;
   uint8_t axis[kMaxPairs]; // axis of each pair
 };
 
+// A lane's 8 values of a row: two runs of 4 elements.
+struct Raw {
+  uint2 lo, hi;
+};
 template <typename T> struct Pack;
 template <> struct Pack<__half> {
-  static __device__ __forceinline__ void load(const uint4& v, float (&f)[8]) {
-    const __half2* h = reinterpret_cast<const __half2*>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = __half22float2(h[i]);
-      f[2 * i] = t.x; f[2 * i + 1] = t.y;
-    }
+  static __device__ __forceinline__ void load2(uint32_t w, float& a, float& b) {
+    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    a = t.x; b = t.y;
   }
-  static __device__ __forceinline__ uint4 store(const float (&f)[8]) {
-    uint4 v;
-    __half2* h = reinterpret_cast<__half2*>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-    return v;
+  static __device__ __forceinline__ uint32_t store2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
   static __device__ __forceinline__ __half one(float x) { return __float2half_rn(x); }
 };
 template <> struct Pack<__nv_bfloat16> {
-  static __device__ __forceinline__ void load(const uint4& v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+  static __device__ __forceinline__ void load2(uint32_t w, float& a, float& b) {
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xffff0000u);
   }
-  static __device__ __forceinline__ uint4 store(const float (&f)[8]) {
-    uint4 v;
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    return v;
+  static __device__ __forceinline__ uint32_t store2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
   static __device__ __forceinline__ __nv_bfloat16 one(float x) { return __float2bfloat16_rn(x); }
 };
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw& r, float (&f)[8]) {
+  Pack<T>::load2(r.lo.x, f[0], f[1]);
+  Pack<T>::load2(r.lo.y, f[2], f[3]);
+  Pack<T>::load2(r.hi.x, f[4], f[5]);
+  Pack<T>::load2(r.hi.y, f[6], f[7]);
+}
+
+// Which elements a lane holds: 4 from lo and 4 from hi.  Interleaved pairs are
+// neighbours, so a run of 8; else the pairs (i, i + rot / 2) of 4 values of i,
+// and runs of 8 of what is not rotated.
+struct Elements {
+  int lo, hi, pair;     // pair: the first of the lane's pairs, or -1
+};
+template <bool INTERLEAVED>
+__device__ __forceinline__ Elements elements(int rot, int sub) {
+  if (INTERLEAVED || sub * 8 >= rot) return Elements{sub * 8, sub * 8 + 4, sub * 8 < rot ? sub * 4 : -1};
+  return Elements{sub * 4, rot / 2 + sub * 4, sub * 4};
+}
+__device__ __forceinline__ Raw load_row(const uint16_t* row, const Elements& e) {
+  return Raw{*reinterpret_cast<const uint2*>(row + e.lo), *reinterpret_cast<const uint2*>(row + e.hi)};
+}
+template <typename T>
+__device__ __forceinline__ void store_row(uint16_t* row, const Elements& e, const float (&f)[8]) {
+  *reinterpret_cast<uint2*>(row + e.lo) = make_uint2(Pack<T>::store2(f[0], f[1]), Pack<T>::store2(f[2], f[3]));
+  *reinterpret_cast<uint2*>(row + e.hi) = make_uint2(Pack<T>::store2(f[4], f[5]), Pack<T>::store2(f[6], f[7]));
+}
 
 // Sum over the LANES lanes that hold one head vector.
 template <int LANES>
@@ -98,145 +117,147 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// This lane's cosines and (signed) sines of one token: value e turns as
-// e * cs[.] + partner * sn[.].
-template <bool INTERLEAVED>
+// A frequency in radians as a fraction of a turn in units of 2^-64, modulo a
+// turn.  With f = m 2^(e - 63), m in [2^63, 2^64), and K = 2^66 / (2 pi):
+// f / (2 pi) 2^64 = (m K 2^-64) 2^(e - 1).
+__device__ __forceinline__ uint64_t turns_of(double f) {
+  const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(f));
+  const int e = static_cast<int>((bits >> 52) & 0x7ff) - 1023;
+  const uint64_t m = (bits << 11) | (1ull << 63), K = 0xA2F9836E4E44152Aull;
+  const uint64_t hi = __umul64hi(m, K);
+  uint64_t fixed = 0ull;               // zero and tiny; 2^64 and more, infinite and NaN
+  if (e <= 1 && e > -63) fixed = hi >> (1 - e);
+  if (e > 1 && e <= 64) fixed = (hi << (e - 1)) | ((m * K) >> (65 - e));
+  return (bits >> 63) ? 0ull - fixed : fixed;
+}
+
+// cos and sin of pair i of a token.
+__device__ __forceinline__ float2 angle(const RopeParams& p, int64_t token, int i) {
+  const int64_t pos = p.positions[p.axis[i] * (p.B * p.S) + token];
+  // The product modulo 2^64 is the angle modulo a turn; its top half as a
+  // signed number counts half turns of 2^-31.
+  const int32_t half_turns = static_cast<int32_t>((static_cast<uint64_t>(pos) * turns_of(p.inv_freq[i])) >> 32);
+  float s, c;
+  sincospif(static_cast<float>(half_turns) * 4.656612873077392578125e-10f, &s, &c);
+  return make_float2(c, s);
+}
+
+// The cosines and sines of a block's tokens, a pair a thread.
+__device__ __forceinline__ void block_angles(const RopeParams& p, int64_t token0, float2 (*table)[kMaxPairs]) {
+  const int i = threadIdx.x % kMaxPairs;
+  if (i >= p.rot / 2) return;
+  for (int k = threadIdx.x / kMaxPairs; k < kWarps / p.share; k += kWarps * 32 / kMaxPairs)
+    if (token0 + k < p.B * p.S) table[k][i] = angle(p, token0 + k, i);
+}
+
+// A lane's four pairs: cosines and sines (turned back with direction -1).
 struct Turn {
-  static constexpr int N = INTERLEAVED ? 4 : 8;   // pairs that a lane's 8 values touch
-  float cs[N], sn[N];
+  float cs[4], sn[4];
 };
-
-// cos and sin of the token's pairs into table[0 .. rot / 2), by the warp.
-__device__ __forceinline__ void angles(const RopeParams& p, int64_t token, float2* table, int lane) {
-  const int64_t tokens = p.B * p.S;
+__device__ __forceinline__ Turn load_turn(const float2* table, const Elements& e, float direction) {
+  Turn t;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int i = lane + 32 * j;
-    if (i < p.rot / 2) {
-      double turns = p.inv_freq[i] * 0.15915494309189534561;   // 1 / (2 pi)
-      turns -= floor(turns);
-      const uint64_t fixed = (turns >= 0.0 && turns < 1.0) ? __double2ull_rn(turns * 18446744073709551616.0) : 0ull;
-      const int64_t pos = p.positions[p.axis[i] * tokens + token];
-      // The product modulo 2^64 is the angle modulo a turn; its top half as a
-      // signed number counts half turns of 2^-31.
-      const int32_t half_turns = static_cast<int32_t>((static_cast<uint64_t>(pos) * fixed) >> 32);
-      float s, c;
-      sincospif(static_cast<float>(half_turns) * 4.656612873077392578125e-10f, &s, &c);
-      table[i] = make_float2(c, s);
-    }
-  }
-}
-
-// The lane's turn from the table; sub: lane within the head's lanes.  Values
-// that are not rotated turn by nothing (cos 1, sin 0, own value as partner).
-template <bool INTERLEAVED>
-__device__ __forceinline__ void load_turn(const RopeParams& p, const float2* table, int sub,
-                                          float direction, Turn<INTERLEAVED>& t) {
-  const int e0 = sub * 8;
-#pragma unroll
-  for (int j = 0; j < Turn<INTERLEAVED>::N; ++j) {
-    float2 v = make_float2(1.0f, 0.0f);
-    float sign = direction;
-    if (e0 < p.rot) {
-      if (INTERLEAVED) {
-        v = table[e0 / 2 + j];
-      } else {
-        const bool upper = e0 >= p.rot / 2;
-        v = table[(upper ? e0 - p.rot / 2 : e0) + j];
-        sign = upper ? direction : -direction;
-      }
-    }
+  for (int j = 0; j < 4; ++j) {
+    const float2 v = e.pair >= 0 ? table[e.pair + j] : make_float2(1.0f, 0.0f);
     t.cs[j] = v.x;
-    t.sn[j] = sign * v.y;
+    t.sn[j] = direction * v.y;
   }
+  return t;
 }
-
 template <bool INTERLEAVED>
-__device__ __forceinline__ void turn(float (&y)[8], const Turn<INTERLEAVED>& t, int partner) {
-  if (INTERLEAVED) {
+__device__ __forceinline__ void turn(float (&y)[8], const Turn& t) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = y[2 * j], b = y[2 * j + 1];
-      y[2 * j] = a * t.cs[j] - b * t.sn[j];
-      y[2 * j + 1] = b * t.cs[j] + a * t.sn[j];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float o = __shfl_sync(0xffffffffu, y[j], partner);
-      y[j] = y[j] * t.cs[j] + o * t.sn[j];
-    }
+  for (int j = 0; j < 4; ++j) {
+    float& a = y[INTERLEAVED ? 2 * j : j];
+    float& b = y[INTERLEAVED ? 2 * j + 1 : j + 4];
+    const float x = a * t.cs[j] - b * t.sn[j];
+    b = b * t.cs[j] + a * t.sn[j];
+    a = x;
   }
 }
 
-// The lane whose values are this lane's partners.
-__device__ __forceinline__ int partner_lane(const RopeParams& p, int lane, int sub) {
-  const int e0 = sub * 8;
-  if (e0 >= p.rot) return lane;
-  const int d = p.rot / 16;
-  return e0 < p.rot / 2 ? lane + d : lane - d;
-}
-
-template <typename T>
-__device__ __forceinline__ void load_weight(const RopeParams& p, int which, int sub, float (&w)[8]) {
-  if (p.weight[which]) {
-    uint4 v;
-    const uint16_t* src = static_cast<const uint16_t*>(p.weight[which]) + sub * 8;
-    uint16_t* dst = reinterpret_cast<uint16_t*>(&v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dst[j] = src[j];   // a weight vector may start anywhere
-    Pack<T>::load(v, w);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+// Both weight vectors as fp32 in shared memory (ones where there is none), by the block.
+template <typename T, int D>
+__device__ __forceinline__ void block_weights(const RopeParams& p, float (*table)[D]) {
+  for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) {
+    const T* src = static_cast<const T*>(p.weight[i / D]);
+    table[i / D][i % D] = src ? static_cast<float>(src[i % D]) : 1.0f;
   }
+}
+__device__ __forceinline__ void load_weight(const float* table, const Elements& e, float (&w)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(table + e.lo), b = *reinterpret_cast<const float4*>(table + e.hi);
+  w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+  w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 
 __device__ __forceinline__ int64_t row_base(const fa_strides_t& st, int64_t b, int64_t s) {
   return b * st.batch + s * st.seq;
 }
 
-constexpr int kFwdRows = 4;   // rows in flight a lane
+// A warp's heads of one kind, [first, last): its part of the token's list of
+// query heads and then key heads, PER at a time.
+template <int PER>
+__device__ __forceinline__ void heads_of(const RopeParams& p, int part, int which, int& first, int& last) {
+  const int nq = (p.heads[0] + PER - 1) / PER, nk = (p.heads[1] + PER - 1) / PER;
+  const int a = (nq + nk) * part / p.share, b = (nq + nk) * (part + 1) / p.share;
+  first = PER * (which ? max(a - nq, 0) : min(a, nq));
+  last = min(PER * (which ? max(b - nq, 0) : min(b, nq)), p.heads[which]);
+}
+
+constexpr int kFwdRows = 2;   // rows a lane loads ahead
 
 template <typename T, int D, bool INTERLEAVED, bool NORM>
-__global__ void __launch_bounds__(kWarps * 32) fa_rope_fwd_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 4) fa_rope_fwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LANES = D / 8, PER = 32 / LANES;   // lanes a head, heads a warp at once
-  __shared__ float2 tables[kWarps][kMaxPairs];
+  __shared__ float2 table[kWarps][kMaxPairs];
+  __shared__ __align__(16) float weights[2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % LANES, slot = lane / LANES;
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  const int64_t token = task / p.parts;
-  const int part = static_cast<int>(task - token * p.parts);
-  if (token >= p.B * p.S) return;
-  const int64_t b = token / p.S, s = token - b * p.S;
+  fa::wait_for_stream();
+  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * (kWarps / p.share);
+  const int mine = warp / p.share, part = warp % p.share;
+  const bool real = token0 + mine < p.B * p.S;
+  const uint32_t token = real ? static_cast<uint32_t>(token0 + mine) : 0u;
+  const uint32_t b = token / static_cast<uint32_t>(p.S), s = token - b * static_cast<uint32_t>(p.S);
+  const Elements e = elements<INTERLEAVED>(p.rot, sub);
 
-  if (p.rot > 0) angles(p, token, tables[warp], lane);
-  __syncwarp();
-  Turn<INTERLEAVED> t;
-  load_turn<INTERLEAVED>(p, tables[warp], sub, 1.0f, t);
-  const int partner = partner_lane(p, lane, sub);
-
+  Turn t;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    float w[8];
-    if (NORM) load_weight<T>(p, which, sub, w);
-    const uint16_t* src = static_cast<const uint16_t*>(p.x[which]) + row_base(p.st_x[which], b, s) + sub * 8;
-    uint16_t* dst = static_cast<uint16_t*>(p.out[which]) + row_base(p.st_out[which], b, s) + sub * 8;
-    const int stride = PER * p.parts;
-    for (int h0 = part * PER; h0 < p.heads[which]; h0 += stride * kFwdRows) {
-      uint4 raw[kFwdRows];
+    int first, last;
+    heads_of<PER>(p, part, which, first, last);
+    if (!real) last = 0;
+    const int64_t x_step = p.st_x[which].head, out_step = p.st_out[which].head;
+    const uint16_t* src = static_cast<const uint16_t*>(p.x[which]) + row_base(p.st_x[which], b, s);
+    uint16_t* dst = static_cast<uint16_t*>(p.out[which]) + row_base(p.st_out[which], b, s);
+    Raw raw[kFwdRows];
+    auto load = [&](int h0) {
 #pragma unroll
       for (int i = 0; i < kFwdRows; ++i) {
-        const int h = h0 + i * stride + slot;
-        raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (h < p.heads[which]) raw[i] = *reinterpret_cast<const uint4*>(src + h * p.st_x[which].head);
+        const int h = h0 + i * PER + slot;
+        raw[i] = Raw{};
+        if (h < last) raw[i] = load_row(src + h * x_step, e);
       }
+    };
+    load(first);
+    if (which == 0) {
+      if (NORM) block_weights<T, D>(p, weights);
+      block_angles(p, token0, table);
+      __syncthreads();
+      t = load_turn(table[mine], e, 1.0f);
+    }
+    float w[8];
+    if (NORM) load_weight(weights[which], e, w);
+    for (int h0 = first; h0 < last; h0 += PER * kFwdRows) {
+      Raw now[kFwdRows];
+#pragma unroll
+      for (int i = 0; i < kFwdRows; ++i) now[i] = raw[i];
+      load(h0 + PER * kFwdRows);
 #pragma unroll
       for (int i = 0; i < kFwdRows; ++i) {
-        if (h0 + i * stride >= p.heads[which]) break;   // the same for the whole warp
-        const int h = h0 + i * stride + slot;
+        const int h = h0 + i * PER + slot;
         float y[8];
-        Pack<T>::load(raw[i], y);
+        unpack<T>(now[i], y);
         if (NORM) {
           float ss = 0.0f;
 #pragma unroll
@@ -245,9 +266,8 @@ __global__ void __launch_bounds__(kWarps * 32) fa_rope_fwd_kernel(const __grid_c
 #pragma unroll
           for (int j = 0; j < 8; ++j) y[j] = y[j] * r * w[j];
         }
-        turn<INTERLEAVED>(y, t, partner);
-        if (h < p.heads[which])
-          *reinterpret_cast<uint4*>(dst + h * p.st_out[which].head) = Pack<T>::store(y);
+        turn<INTERLEAVED>(y, t);
+        if (h < last) store_row<T>(dst + h * out_step, e, y);
       }
     }
   }
@@ -256,56 +276,71 @@ __global__ void __launch_bounds__(kWarps * 32) fa_rope_fwd_kernel(const __grid_c
 constexpr int kBwdRows = 2;
 
 template <typename T, int D, bool INTERLEAVED, bool NORM>
-__global__ void __launch_bounds__(kWarps * 32) fa_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kBwdResident) fa_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LANES = D / 8, PER = 32 / LANES;
-  __shared__ float2 tables[kWarps][kMaxPairs];
+  __shared__ float2 table[2][kWarps][kMaxPairs];
+  __shared__ __align__(16) float weights[2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % LANES, slot = lane / LANES;
-  const int partner = partner_lane(p, lane, sub);
-  const int64_t tasks = p.B * p.S * p.parts;
+  fa::wait_for_stream();
+  const Elements e = elements<INTERLEAVED>(p.rot, sub);
+  const int per_block = kWarps / p.share, mine = warp / p.share, part = warp % p.share;
+  const int64_t tokens = p.B * p.S;
   float dw[2][8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) dw[i / 8][i % 8] = 0.0f;
+  for (int j = 0; j < 16; ++j) dw[j / 8][j % 8] = 0.0f;
 
-  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + warp; task < tasks;
-       task += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t token = task / p.parts;
-    const int part = static_cast<int>(task - token * p.parts);
-    const int64_t b = token / p.S, s = token - b * p.S;
-    __syncwarp();                                 // the last task's table has been read
-    if (p.rot > 0) angles(p, token, tables[warp], lane);
-    __syncwarp();
-    Turn<INTERLEAVED> t;
-    load_turn<INTERLEAVED>(p, tables[warp], sub, -1.0f, t);
+  if (NORM) block_weights<T, D>(p, weights);      // (read behind the first barrier)
+  int buffer = 0;
+  for (int64_t token0 = static_cast<int64_t>(blockIdx.x) * per_block; token0 < tokens;
+       token0 += static_cast<int64_t>(gridDim.x) * per_block, buffer ^= 1) {
+    const bool real = token0 + mine < tokens;
+    const uint32_t token = real ? static_cast<uint32_t>(token0 + mine) : 0u;
+    const uint32_t b = token / static_cast<uint32_t>(p.S), s = token - b * static_cast<uint32_t>(p.S);
+    Turn t;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-      float w[8];
-      if (NORM) load_weight<T>(p, which, sub, w);
-      const uint16_t* x = static_cast<const uint16_t*>(p.x[which]) + row_base(p.st_x[which], b, s) + sub * 8;
-      const uint16_t* dy = static_cast<const uint16_t*>(p.dy[which]) + row_base(p.st_dy[which], b, s) + sub * 8;
-      uint16_t* dst = static_cast<uint16_t*>(p.out[which]) + row_base(p.st_out[which], b, s) + sub * 8;
-      const int stride = PER * p.parts;
-      for (int h0 = part * PER; h0 < p.heads[which]; h0 += stride * kBwdRows) {
-        uint4 rx[kBwdRows], rg[kBwdRows];
+      int first, last;
+      heads_of<PER>(p, part, which, first, last);
+      if (!real) last = 0;
+      const int64_t x_step = p.st_x[which].head, dy_step = p.st_dy[which].head, out_step = p.st_out[which].head;
+      const uint16_t* x = static_cast<const uint16_t*>(p.x[which]) + row_base(p.st_x[which], b, s);
+      const uint16_t* dy = static_cast<const uint16_t*>(p.dy[which]) + row_base(p.st_dy[which], b, s);
+      uint16_t* dst = static_cast<uint16_t*>(p.out[which]) + row_base(p.st_out[which], b, s);
+      Raw rx[kBwdRows], rg[kBwdRows];
+      auto load = [&](int h0) {
 #pragma unroll
         for (int i = 0; i < kBwdRows; ++i) {
-          const int h = h0 + i * stride + slot;
-          rx[i] = rg[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (h < p.heads[which]) {
-            rg[i] = *reinterpret_cast<const uint4*>(dy + h * p.st_dy[which].head);
-            if (NORM) rx[i] = *reinterpret_cast<const uint4*>(x + h * p.st_x[which].head);
+          const int h = h0 + i * PER + slot;
+          rx[i] = rg[i] = Raw{};
+          if (h < last) {
+            rg[i] = load_row(dy + h * dy_step, e);
+            if (NORM) rx[i] = load_row(x + h * x_step, e);
           }
         }
+      };
+      load(first);
+      if (which == 0) {       // (the other buffer's readers have passed this barrier since)
+        block_angles(p, token0, table[buffer]);
+        __syncthreads();
+        t = load_turn(table[buffer][mine], e, -1.0f);
+      }
+      float w[8];
+      if (NORM) load_weight(weights[which], e, w);
+      for (int h0 = first; h0 < last; h0 += PER * kBwdRows) {
+        Raw nx[kBwdRows], ng[kBwdRows];
+#pragma unroll
+        for (int i = 0; i < kBwdRows; ++i) { nx[i] = rx[i]; ng[i] = rg[i]; }
+        load(h0 + PER * kBwdRows);
 #pragma unroll
         for (int i = 0; i < kBwdRows; ++i) {
-          if (h0 + i * stride >= p.heads[which]) break;
-          const int h = h0 + i * stride + slot;
+          const int h = h0 + i * PER + slot;
           float g[8];
-          Pack<T>::load(rg[i], g);
-          turn<INTERLEAVED>(g, t, partner);
+          unpack<T>(ng[i], g);
+          turn<INTERLEAVED>(g, t);
           if (NORM) {
             float xv[8];
-            Pack<T>::load(rx[i], xv);
+            unpack<T>(nx[i], xv);
             float ss = 0.0f, dot = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -314,9 +349,9 @@ __global__ void __launch_bounds__(kWarps * 32) fa_rope_bwd_kernel(const __grid_c
             }
             const float r = rsqrtf(head_sum<LANES>(ss) * (1.0f / D) + p.eps);
             const float c = head_sum<LANES>(dot) * (1.0f / D) * r * r;
-            // h < heads only: a lane without a row holds zeros, which add
+            // h < last only: a lane without a row holds zeros, which add
             // nothing to dw unless r is infinite (0 * inf)
-            if (h < p.heads[which]) {
+            if (h < last) {
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 dw[which][j] += g[j] * xv[j] * r;
@@ -324,15 +359,14 @@ __global__ void __launch_bounds__(kWarps * 32) fa_rope_bwd_kernel(const __grid_c
               }
             }
           }
-          if (h < p.heads[which])
-            *reinterpret_cast<uint4*>(dst + h * p.st_out[which].head) = Pack<T>::store(g);
+          if (h < last) store_row<T>(dst + h * out_step, e, g);
         }
       }
     }
   }
 
   if (NORM && p.partial) {
-    // The block's sums in a fixed order: lanes of the same elements, warps.
+    // The block's sums in a fixed order: lanes of the same elements, then warps.
     __shared__ float sums[kWarps][2][D];
 #pragma unroll
     for (int which = 0; which < 2; ++which)
@@ -341,7 +375,7 @@ __global__ void __launch_bounds__(kWarps * 32) fa_rope_bwd_kernel(const __grid_c
         float v = dw[which][j];
 #pragma unroll
         for (int o = LANES; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (slot == 0) sums[warp][which][sub * 8 + j] = v;
+        if (slot == 0) sums[warp][which][j < 4 ? e.lo + j : e.hi + j - 4] = v;
       }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) {
@@ -354,24 +388,25 @@ __global__ void __launch_bounds__(kWarps * 32) fa_rope_bwd_kernel(const __grid_c
 }
 
 // Weight gradients: element i of both vectors over the blocks' partial sums,
-// eight threads an element; grid 2 D / 32 blocks of 256 threads.
+// 32 threads an element; 2 D / 32 blocks of 1024 threads.
 template <typename T>
-__global__ void __launch_bounds__(256) fa_rope_dw_kernel(const float* partial, int blocks, int D,
-                                                         T* dwq, T* dwk) {
-  __shared__ float sums[8][32];
+__global__ void __launch_bounds__(1024) fa_rope_dw_kernel(const float* partial, int blocks, int D,
+                                                          T* dwq, T* dwk) {
+  __shared__ float sums[32][33];
+  fa::wait_for_stream();
   const int e = threadIdx.x & 31, k = threadIdx.x >> 5;
-  const int i = blockIdx.x * 32 + e;     // of 2 D
+  const float* src = partial + blockIdx.x * 32 + e;     // element of 2 D
   float v = 0.0f;
-  for (int r = k; r < blocks; r += 8) v += partial[static_cast<int64_t>(r) * 2 * D + i];
+#pragma unroll 4
+  for (int r = k; r < blocks; r += 32) v += src[static_cast<int64_t>(r) * 2 * D];
   sums[k][e] = v;
   __syncthreads();
-  if (k == 0) {
-    v = 0.0f;
+  v = sums[e][k];                                       // warp k: element k
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v += sums[j][e];
-    T* out = i < D ? dwq : dwk;
-    if (out) out[i < D ? i : i - D] = Pack<T>::one(v);
-  }
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int i = blockIdx.x * 32 + k;
+  T* out = i < D ? dwq : dwk;
+  if (e == 0 && out) out[i < D ? i : i - D] = Pack<T>::one(v);
 }
 
 bool off(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
@@ -455,7 +490,7 @@ fa_status_t check_common(int64_t B, int64_t S, int64_t H, int64_t H_kv, int64_t 
     for (int64_t i = 0; i < rot / 2; ++i)
       if (pair_axis[i] >= n_axes) return FA_ERR_INVALID_ARG;
   if (H > (1 << 20) || H_kv > (1 << 20)) return FA_ERR_UNSUPPORTED;
-  if (B > 0 && S > 0 && S > (int64_t(1) << 40) / B) return FA_ERR_UNSUPPORTED;
+  if (B > 0 && S > 0 && S > ((int64_t(1) << 31) - 1) / B) return FA_ERR_UNSUPPORTED;
   if (off(positions, 4) || off(inv_freq, 8) || off(qw, 2) || off(kw, 2)) return FA_ERR_MISALIGNED;
   return FA_OK;
 }
@@ -487,30 +522,21 @@ void fill(RopeParams& p, const int32_t* positions, const double* inv_freq, int64
   if (pair_axis) std::memcpy(p.axis, pair_axis, static_cast<size_t>(rot / 2));
 }
 
-// Warps a token: enough tasks for 16 warps on each of 152 SMs, each with one
-// pass over the query heads at least.
-int parts_for(int64_t tokens, int64_t H, int per) {
-  const int64_t passes = std::max<int64_t>(1, (H + per - 1) / per);
-  const int64_t want = (152 * 16 + tokens - 1) / tokens;
-  return static_cast<int>(std::max<int64_t>(1, std::min(want, passes)));
-}
-
-cudaLaunchConfig_t config(int64_t grid, int threads, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(threads);
-  cfg.stream = stream;
-  return cfg;
+// Warps that share a token: more while the tokens alone would not give each of
+// 152 SMs its 32 warps (backward: 16).  At 16384 tokens, 32 + 8 heads of 128:
+// forward 60.0 us with one, 60.7 with two, 74.7 with four.
+int share_for(int64_t tokens) {
+  return tokens >= 152 * 64 ? 1 : tokens >= 152 * 16 ? 2 : tokens >= 152 * 8 ? 4 : 8;
 }
 
 template <typename T, int D>
 cudaError_t launch_fwd(const RopeParams& p, bool interleaved, bool norm, int64_t grid, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = config(grid, kWarps * 32, stream);
+  const fa::Launch c(dim3(static_cast<unsigned>(grid)), kWarps * 32, 0, stream);
   if (interleaved)
-    return norm ? cudaLaunchKernelEx(&cfg, fa_rope_fwd_kernel<T, D, true, true>, p)
-                : cudaLaunchKernelEx(&cfg, fa_rope_fwd_kernel<T, D, true, false>, p);
-  return norm ? cudaLaunchKernelEx(&cfg, fa_rope_fwd_kernel<T, D, false, true>, p)
-              : cudaLaunchKernelEx(&cfg, fa_rope_fwd_kernel<T, D, false, false>, p);
+    return norm ? cudaLaunchKernelEx(&c.cfg, fa_rope_fwd_kernel<T, D, true, true>, p)
+                : cudaLaunchKernelEx(&c.cfg, fa_rope_fwd_kernel<T, D, true, false>, p);
+  return norm ? cudaLaunchKernelEx(&c.cfg, fa_rope_fwd_kernel<T, D, false, true>, p)
+              : cudaLaunchKernelEx(&c.cfg, fa_rope_fwd_kernel<T, D, false, false>, p);
 }
 
 template <typename T, int D>
@@ -518,17 +544,17 @@ cudaError_t launch_bwd(const RopeParams& p, bool interleaved, bool norm, int64_t
                        void* dwk, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (grid > 0) {
-    cudaLaunchConfig_t cfg = config(grid, kWarps * 32, stream);
+    const fa::Launch c(dim3(static_cast<unsigned>(grid)), kWarps * 32, 0, stream);
     if (interleaved)
-      e = norm ? cudaLaunchKernelEx(&cfg, fa_rope_bwd_kernel<T, D, true, true>, p)
-               : cudaLaunchKernelEx(&cfg, fa_rope_bwd_kernel<T, D, true, false>, p);
+      e = norm ? cudaLaunchKernelEx(&c.cfg, fa_rope_bwd_kernel<T, D, true, true>, p)
+               : cudaLaunchKernelEx(&c.cfg, fa_rope_bwd_kernel<T, D, true, false>, p);
     else
-      e = norm ? cudaLaunchKernelEx(&cfg, fa_rope_bwd_kernel<T, D, false, true>, p)
-               : cudaLaunchKernelEx(&cfg, fa_rope_bwd_kernel<T, D, false, false>, p);
+      e = norm ? cudaLaunchKernelEx(&c.cfg, fa_rope_bwd_kernel<T, D, false, true>, p)
+               : cudaLaunchKernelEx(&c.cfg, fa_rope_bwd_kernel<T, D, false, false>, p);
   }
   if (e != cudaSuccess || !(dwq || dwk)) return e;
-  cudaLaunchConfig_t cfg = config(2 * D / 32, 256, stream);
-  return cudaLaunchKernelEx(&cfg, fa_rope_dw_kernel<T>, static_cast<const float*>(p.partial),
+  const fa::Launch c(dim3(2 * D / 32), 1024, 0, stream);
+  return cudaLaunchKernelEx(&c.cfg, fa_rope_dw_kernel<T>, static_cast<const float*>(p.partial),
                             static_cast<int>(grid), D, static_cast<T*>(dwq), static_cast<T*>(dwk));
 }
 
@@ -564,9 +590,9 @@ fa_status_t fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_o
   p.out[0] = q_out; p.out[1] = k_out;
   for (int i = 0; i < 2; ++i) { p.st_x[i] = strides[i]; p.st_out[i] = strides[2 + i]; }
   fill(p, positions, inv_freq, B, S, H, H_kv, rot_dim, pair_axis, eps, q_weight, k_weight);
-  p.parts = parts_for(B * S, H, static_cast<int>(256 / D));
-  const int64_t grid = (B * S * p.parts + kWarps - 1) / kWarps;
-  if (grid > INT32_MAX) return FA_ERR_UNSUPPORTED;
+  p.share = share_for(B * S);
+  const int per_block = kWarps / p.share;
+  const int64_t grid = (B * S + per_block - 1) / per_block;
   cudaError_t e;
   if (dtype == FA_DTYPE_F16)
     e = D == 64 ? launch_fwd<__half, 64>(p, interleaved, norm, grid, stream)
@@ -631,8 +657,9 @@ fa_status_t fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const vo
   p.partial = want_dw ? static_cast<float*>(workspace) : nullptr;
   int64_t grid = 0;
   if (!empty) {
-    p.parts = parts_for(B * S, H, static_cast<int>(256 / D));
-    grid = std::min<int64_t>((B * S * p.parts + kWarps - 1) / kWarps, kBwdBlocks);
+    p.share = share_for(B * S);
+    const int per_block = kWarps / p.share;
+    grid = std::min<int64_t>((B * S + per_block - 1) / per_block, kBwdBlocks);
   }
   cudaError_t e;
   if (dtype == FA_DTYPE_F16)

@@ -16,6 +16,7 @@
 #include <cstdint>
 
 #include "../../include/fa_api.h"
+#include "fa_launch.cuh"
 
 namespace {
 
@@ -74,6 +75,7 @@ __global__ void __launch_bounds__(kThreads) fa_slots_kernel(const SlotParams p) 
   __shared__ int64_t warp_rows[kThreads / 32], warp_pages[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = p.n_seqs;
+  fa::wait_for_stream();
 
   // Running sums: each thread a contiguous run of requests, then the runs.
   const int per = (n + kThreads - 1) / kThreads;
@@ -209,10 +211,6 @@ extern "C" fa_status_t fa_paged_slots(const int32_t* past_k, const int32_t* new_
   // A block for 512 rows, at most one on each of 152 SMs: more would repeat
   // the sums without spreading the rows any further.
   const int64_t want = (std::max(total_q, n_seqs) + kThreads - 1) / kThreads;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(want, 152)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, fa_slots_kernel, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const fa::Launch c(dim3(static_cast<unsigned>(std::min<int64_t>(want, 152))), kThreads, smem, stream);
+  return cudaLaunchKernelEx(&c.cfg, fa_slots_kernel, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -13,30 +13,52 @@ device, does not synchronise, and can be captured into a CUDA graph.
 """
 from __future__ import annotations
 
-import contextlib
 import math
+import struct
 from typing import NamedTuple
 
 import torch
 
-from .binding import CAUSAL, FA_DTYPE, FaError, fa_fwd_paged_kv4_workspace_size, load, Strides
+from .binding import CAUSAL, FA_DTYPE, FaError, fa_fwd_paged_kv4_workspace_size, load
 
+_I32, _I64, _U8 = torch.int32, torch.int64, torch.uint8
 _DTYPE = {torch.float16: FA_DTYPE["f16"], torch.bfloat16: FA_DTYPE["bf16"]}
+_two_strides = struct.Struct("6q").pack     # two fa_strides_t
 
 
-def _on(device):
-    """The device guard of a call (nothing to do on the current device)."""
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _stream(index):
+    """The current stream of a device (torch.cuda.current_stream without the object)."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _check(name, t, dtype, shape, device):
-    """A dense CUDA tensor of this type and shape on this device (None: any size)."""
+
+# A decoding step makes several of these calls in the time its kernels take, so
+# the checks are single expressions over cheap attributes; only a failed one
+# goes through _check, which says what is wrong.
+
+
+def _call(name, fn, index, *args):
+    """fn(*args, stream) with device `index` current, on its current stream."""
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, _stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _stream(index))
+    if st != 0:
+        raise FaError(st, name)
+
+
+def _is(t, dtype, shape, index):
+    return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
+
+
+def _check(name, t, dtype, shape, index):
+    """Raises unless t is a dense tensor of this type and shape (None: any size) on CUDA
+    device `index`."""
     if t.dtype != dtype:
         raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{max(index, 0)}")
     if len(t.shape) != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
@@ -44,9 +66,10 @@ def _check(name, t, dtype, shape, device):
 
 
 def _dtype_of(name, t):
-    if t.dtype not in _DTYPE:
+    code = _DTYPE.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    return _DTYPE[t.dtype]
+    return code
 
 
 class PagedSlots(NamedTuple):
@@ -67,32 +90,30 @@ def paged_slots(past_k, new_q, free_pages, block_table, *, page_size, total_q, o
     (at least the sum of new_q; rows behind it get slot -1, position 0).  `out`:
     a PagedSlots to write into.  pages_taken above free_pages' length says that
     the list ran out (the tokens without a page have slot -1)."""
-    dev = past_k.device
-    n = past_k.shape[0]
-    _check("past_k", past_k, torch.int32, (n,), dev)
-    _check("new_q", new_q, torch.int32, (n,), dev)
-    _check("free_pages", free_pages, torch.int32, (None,), dev)
-    _check("block_table", block_table, torch.int32, (n, None), dev)
+    dev, n = past_k.get_device(), past_k.shape[0]
+    if not (dev >= 0 and _is(past_k, _I32, (n,), dev) and _is(new_q, _I32, (n,), dev)):
+        _check("past_k", past_k, _I32, (n,), dev)
+        _check("new_q", new_q, _I32, (n,), dev)
+    if free_pages.dtype is not _I32 or free_pages.get_device() != dev or free_pages.dim() != 1 or not free_pages.is_contiguous():
+        _check("free_pages", free_pages, _I32, (None,), dev)
+    if block_table.dim() != 2 or not _is(block_table, _I32, (n, block_table.shape[1]), dev):
+        _check("block_table", block_table, _I32, (n, None), dev)
     if out is None:
-        i32 = {"dtype": torch.int32, "device": dev}
+        i32 = {"dtype": _I32, "device": past_k.device}
         out = PagedSlots(torch.empty(n + 1, **i32), torch.empty(n, **i32), torch.empty(total_q, **i32),
-                         torch.empty(total_q, dtype=torch.int64, device=dev), torch.empty(1, **i32))
+                         torch.empty(total_q, dtype=_I64, device=past_k.device), torch.empty(1, **i32))
+        cu, used, pos, slot, taken = out
     else:
-        _check("cu_seqlens_q", out.cu_seqlens_q, torch.int32, (n + 1,), dev)
-        _check("seqused_k", out.seqused_k, torch.int32, (n,), dev)
-        _check("positions", out.positions, torch.int32, (total_q,), dev)
-        _check("slot_map", out.slot_map, torch.int64, (total_q,), dev)
-        _check("pages_taken", out.pages_taken, torch.int32, (1,), dev)
-    with _on(dev):
-        st = load().fa_paged_slots(past_k.data_ptr(), new_q.data_ptr(), free_pages.data_ptr(),
-                                   free_pages.shape[0], block_table.data_ptr(), n,
-                                   block_table.shape[1], page_size, total_q,
-                                   out.cu_seqlens_q.data_ptr(), out.seqused_k.data_ptr(),
-                                   out.positions.data_ptr(), out.slot_map.data_ptr(),
-                                   out.pages_taken.data_ptr(),
-                                   torch.cuda.current_stream(dev).cuda_stream)
-    if st != 0:
-        raise FaError(st, "fa_paged_slots")
+        cu, used, pos, slot, taken = out
+        if not (_is(cu, _I32, (n + 1,), dev) and _is(used, _I32, (n,), dev) and _is(pos, _I32, (total_q,), dev)
+                and _is(slot, _I64, (total_q,), dev) and _is(taken, _I32, (1,), dev)):
+            for name, t, dtype, size in (("cu_seqlens_q", cu, _I32, n + 1), ("seqused_k", used, _I32, n),
+                                         ("positions", pos, _I32, total_q), ("slot_map", slot, _I64, total_q),
+                                         ("pages_taken", taken, _I32, 1)):
+                _check(name, t, dtype, (size,), dev)
+    _call("fa_paged_slots", load().fa_paged_slots, dev, past_k.data_ptr(), new_q.data_ptr(), free_pages.data_ptr(),
+          free_pages.shape[0], block_table.data_ptr(), n, block_table.shape[1], page_size, total_q, cu.data_ptr(),
+          used.data_ptr(), pos.data_ptr(), slot.data_ptr(), taken.data_ptr())
     return out
 
 
@@ -105,20 +126,21 @@ class KV4Cache:
     k_descale, v_descale: floats.  A descale of largest value / (6 * 448) uses
     the scales' whole range."""
 
-    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "k_descale", "v_descale")
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "k_descale", "v_descale", "_geometry")
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, k_descale=1.0, v_descale=1.0):
-        dev = k_codes.device
         if k_codes.dim() != 4:
             raise ValueError(f"k_codes: shape {tuple(k_codes.shape)}, expected [num_pages, H_kv, page_size, D / 2]")
         pages, heads, rows, half = k_codes.shape
+        index = k_codes.get_device()
         for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
-            _check(name, t, torch.uint8, (pages, heads, rows, half), dev)
+            _check(name, t, _U8, (pages, heads, rows, half), index)
         for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-            kind = torch.uint8 if t.dtype == torch.uint8 else torch.float8_e4m3fn
-            _check(name, t, kind, (pages, heads, rows, half // 8), dev)
+            kind = _U8 if t.dtype == _U8 else torch.float8_e4m3fn
+            _check(name, t, kind, (pages, heads, rows, half // 8), index)
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.k_descale, self.v_descale = float(k_descale), float(v_descale)
+        self._geometry = (pages, heads, rows, 2 * half, index)
 
     @classmethod
     def allocate(cls, num_pages, page_size, H_kv, D, device="cuda", k_descale=1.0, v_descale=1.0):
@@ -130,36 +152,35 @@ class KV4Cache:
 
     @property
     def num_pages(self):
-        return self.k_codes.shape[0]
+        return self._geometry[0]
 
     @property
     def H_kv(self):
-        return self.k_codes.shape[1]
+        return self._geometry[1]
 
     @property
     def page_size(self):
-        return self.k_codes.shape[2]
+        return self._geometry[2]
 
     @property
     def D(self):
-        return self.k_codes.shape[3] * 2
+        return self._geometry[3]
 
     @property
     def device(self):
         return self.k_codes.device
 
 
-def _rows(name, t, cache):
-    """Checks rows [n, H_kv, D] with D contiguous; their (batch, head, seq) strides."""
-    n, h, d = t.shape
-    if h != cache.H_kv or d != cache.D:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [n, {cache.H_kv}, {cache.D}]")
-    if t.device != cache.device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+def _rows(name, t, heads, d, index):
+    """The (batch, head, seq) strides of rows t [n, H_kv, D] with D contiguous."""
+    if t.dim() != 3 or t.shape[1:] != (heads, d):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [n, {heads}, {d}]")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
     seq, head, one = t.stride()
     if one != 1:
         raise ValueError(f"{name}: the head dimension must be contiguous")
-    return Strides(1, head if h > 1 else d, seq if n > 1 else h * d)
+    return 1, head if heads > 1 else d, seq if t.shape[0] > 1 else heads * d
 
 
 def kv4_write(k, v, slot_map, cache):
@@ -167,43 +188,37 @@ def kv4_write(k, v, slot_map, cache):
     strides of 16-byte multiples) into the cache's slots slot_map (int64
     [n_tokens]; -1 skips a row, the others must differ)."""
     dt = _dtype_of("k", k)
-    if v.dtype != k.dtype or v.shape != k.shape:
+    pages, heads, rows, d, index = cache._geometry
+    n = k.shape[0]
+    strides = _two_strides(*_rows("k", k, heads, d, index), *_rows("v", v, heads, d, index))
+    if v.dtype is not k.dtype or v.shape[0] != n:
         raise ValueError("k and v must have the same type and shape")
-    dev = cache.device
-    _check("slot_map", slot_map, torch.int64, (k.shape[0],), dev)
-    strides = (Strides * 2)(_rows("k", k, cache), _rows("v", v, cache))
-    pages, heads, rows, half = cache.k_codes.shape
-    with _on(dev):
-        st = load().fa_kv4_write(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), cache.k_codes.data_ptr(),
-                                 cache.k_scales.data_ptr(), cache.v_codes.data_ptr(),
-                                 cache.v_scales.data_ptr(), cache.k_descale, cache.v_descale,
-                                 k.shape[0], heads, 2 * half, rows, pages, strides, dt,
-                                 torch.cuda.current_stream(dev).cuda_stream)
-    if st != 0:
-        raise FaError(st, "fa_kv4_write")
+    if not _is(slot_map, _I64, (n,), index):
+        _check("slot_map", slot_map, _I64, (n,), index)
+    _call("fa_kv4_write", load().fa_kv4_write, index, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(),
+          cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr(),
+          cache.k_descale, cache.v_descale, n, heads, d, rows, pages, strides, dt)
 
 
 def kv4_read(cache, slot_map, dtype=torch.bfloat16, out=None):
     """The rows k, v [n_tokens, H_kv, D] that the cache holds at slot_map, in
     `dtype` (or into `out`, a pair of dense tensors); a slot outside the cache
     reads as zeros."""
-    dev = cache.device
-    pages, heads, rows, half = cache.k_codes.shape
+    pages, heads, rows, d, index = cache._geometry
     n = slot_map.shape[0]
-    _check("slot_map", slot_map, torch.int64, (n,), dev)
+    if not _is(slot_map, _I64, (n,), index):
+        _check("slot_map", slot_map, _I64, (n,), index)
     if out is None:
-        out = tuple(torch.empty(n, heads, 2 * half, dtype=dtype, device=dev) for _ in range(2))
+        out = (torch.empty((n, heads, d), dtype=dtype, device=slot_map.device),
+               torch.empty((n, heads, d), dtype=dtype, device=slot_map.device))
     else:
+        dtype = out[0].dtype
         for name, t in zip(("k", "v"), out):
-            _check(name, t, out[0].dtype, (n, heads, 2 * half), dev)
-    dt = _dtype_of("out", out[0])
-    with _on(dev):
-        st = load().fa_kv4_read(cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(),
-                                cache.v_scales.data_ptr(), slot_map.data_ptr(), out[0].data_ptr(),
-                                out[1].data_ptr(), cache.k_descale, cache.v_descale, n, heads, 2 * half,
-                                rows, pages, dt, torch.cuda.current_stream(dev).cuda_stream)
-    if st != 0:
-        raise FaError(st, "fa_kv4_read")
+            if not _is(t, dtype, (n, heads, d), index):
+                _check(name, t, dtype, (n, heads, d), index)
+    _call("fa_kv4_read", load().fa_kv4_read, index, cache.k_codes.data_ptr(), cache.k_scales.data_ptr(),
+          cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), slot_map.data_ptr(), out[0].data_ptr(),
+          out[1].data_ptr(), cache.k_descale, cache.v_descale, n, heads, d, rows, pages, _dtype_of("out", out[0]))
     return out
 
 
@@ -213,7 +228,7 @@ def paged_attention_kv4_workspace(q, cache, *, max_seqlen_q, n_seqs, total_k):
     st, nbytes = fa_fwd_paged_kv4_workspace_size(n_seqs, max_seqlen_q, total_k, q.shape[1], cache.H_kv, cache.D)
     if st != 0:
         raise FaError(st, "fa_fwd_paged_kv4_workspace_size")
-    return torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+    return torch.empty(nbytes, dtype=_U8, device=cache.device)
 
 
 def paged_attention_kv4(q, cache, cu_seqlens_q, seqused_k, block_table, *, max_seqlen_q, total_k=None,
@@ -228,37 +243,33 @@ def paged_attention_kv4(q, cache, cu_seqlens_q, seqused_k, block_table, *, max_s
     paged_attention_kv4_workspace) saves the allocation; calls that may overlap
     need one each."""
     dt = _dtype_of("q", q)
-    dev = cache.device
-    pages, heads, rows, half = cache.k_codes.shape
-    total_q, H, D = q.shape
-    _check("q", q, q.dtype, (total_q, H, 2 * half), dev)
+    pages, heads, rows, d, index = cache._geometry
+    total_q, H, _ = q.shape
     n, max_pages = block_table.shape
-    _check("cu_seqlens_q", cu_seqlens_q, torch.int32, (n + 1,), dev)
-    _check("seqused_k", seqused_k, torch.int32, (n,), dev)
-    _check("block_table", block_table, torch.int32, (n, max_pages), dev)
+    if not (_is(q, q.dtype, (total_q, H, d), index) and _is(cu_seqlens_q, _I32, (n + 1,), index)
+            and _is(seqused_k, _I32, (n,), index) and _is(block_table, _I32, (n, max_pages), index)):
+        _check("q", q, q.dtype, (total_q, H, d), index)
+        _check("cu_seqlens_q", cu_seqlens_q, _I32, (n + 1,), index)
+        _check("seqused_k", seqused_k, _I32, (n,), index)
+        _check("block_table", block_table, _I32, (n, max_pages), index)
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _check("out", out, q.dtype, (total_q, H, D), dev)
+    elif not _is(out, q.dtype, (total_q, H, d), index):
+        _check("out", out, q.dtype, (total_q, H, d), index)
     if lse is None:
-        lse = torch.empty((H, total_q), dtype=torch.float32, device=dev)
-    else:
-        _check("lse", lse, torch.float32, (H, total_q), dev)
+        lse = torch.empty((H, total_q), dtype=torch.float32, device=q.device)
+    elif not _is(lse, torch.float32, (H, total_q), index):
+        _check("lse", lse, torch.float32, (H, total_q), index)
     if total_k is None:
         total_k = n * max_pages * rows
     if workspace is None:
         workspace = paged_attention_kv4_workspace(q, cache, max_seqlen_q=max_seqlen_q, n_seqs=n, total_k=total_k)
-    else:
-        _check("workspace", workspace, torch.uint8, (None,), dev)
-    with _on(dev):
-        st = load().fa_fwd_paged_kv4(
-            q.data_ptr(), cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(),
-            cache.v_scales.data_ptr(), out.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(),
-            seqused_k.data_ptr(), block_table.data_ptr(), n, max_pages, rows, pages, total_q,
-            max_seqlen_q, total_k, H, heads, D, 1.0 / math.sqrt(D) if scale is None else scale,
-            CAUSAL[causal] if isinstance(causal, str) else int(causal), dt, cache.k_descale,
-            cache.v_descale, workspace.data_ptr(), workspace.shape[0],
-            torch.cuda.current_stream(dev).cuda_stream)
-    if st != 0:
-        raise FaError(st, "fa_fwd_paged_kv4")
+    elif workspace.dim() != 1 or not _is(workspace, _U8, workspace.shape, index):
+        _check("workspace", workspace, _U8, (None,), index)
+    _call("fa_fwd_paged_kv4", load().fa_fwd_paged_kv4, index, q.data_ptr(), cache.k_codes.data_ptr(),
+          cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), out.data_ptr(),
+          lse.data_ptr(), cu_seqlens_q.data_ptr(), seqused_k.data_ptr(), block_table.data_ptr(), n, max_pages, rows,
+          pages, total_q, max_seqlen_q, total_k, H, heads, d, 1.0 / math.sqrt(d) if scale is None else scale,
+          CAUSAL[causal] if isinstance(causal, str) else int(causal), dt, cache.k_descale, cache.v_descale,
+          workspace.data_ptr(), workspace.shape[0])
     return out, lse

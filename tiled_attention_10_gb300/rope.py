@@ -2,76 +2,90 @@
 tensors (fa_qk_norm_rope and its backward; formulas in include/fa_api.h)."""
 from __future__ import annotations
 
+import struct
+
 import torch
 
-from .binding import FaError, Strides, fa_qk_norm_rope_bwd_workspace_size, load
-from .paged import _check, _dtype_of, _on
+from .binding import FaError, fa_qk_norm_rope_bwd_workspace_size, load
+from .paged import _call, _check, _dtype_of, _I32, _is
+
+_F64 = torch.float64
 
 
-class _Shape:
-    """Sizes of q and k in a layout; packed [T, H, D] tensors are one batch, BSND."""
+def _sizes(q, k, layout):
+    """(B, S, H, H_kv, D, sequence dimension before the heads') of q and k in a layout; packed
+    [T, H, D] tensors are one batch."""
+    if q.dim() == 3:
+        (S, H, D), B, bsnd = q.shape, 1, True
+        h_kv = k.shape[1] if k.dim() == 3 else -1
+        want = (S, h_kv, D)
+    elif layout == "BNSD":
+        (B, H, S, D), bsnd = q.shape, False
+        h_kv = k.shape[1]
+        want = (B, h_kv, S, D)
+    elif layout == "BSND":
+        (B, S, H, D), bsnd = q.shape, True
+        h_kv = k.shape[2] if k.dim() == 4 else -1
+        want = (B, S, h_kv, D)
+    else:
+        raise ValueError(f"layout {layout!r}: BNSD or BSND")
+    if k.shape != want:
+        raise ValueError(f"k: shape {tuple(k.shape)} does not go with q's {tuple(q.shape)}")
+    if k.dtype is not q.dtype:
+        raise TypeError(f"k: {k.dtype}, q: {q.dtype}")
+    if not q.is_cuda or k.get_device() != q.get_device():
+        raise ValueError(f"q is on {q.device}, k on {k.device}: one CUDA device expected")
+    return B, S, H, h_kv, D, bsnd
 
-    __slots__ = ("B", "S", "H", "H_kv", "D", "bnsd")
 
-    def __init__(self, q, k, layout):
-        if q.dim() == 3:
-            self.B, (self.S, self.H, self.D), self.bnsd = 1, q.shape, False
-            want, self.H_kv = (self.S, None, self.D), k.shape[1]
-        elif layout == "BNSD":
-            (self.B, self.H, self.S, self.D), self.bnsd = q.shape, True
-            want, self.H_kv = (self.B, None, self.S, self.D), k.shape[1]
-        elif layout == "BSND":
-            (self.B, self.S, self.H, self.D), self.bnsd = q.shape, False
-            want, self.H_kv = (self.B, self.S, None, self.D), k.shape[2]
-        else:
-            raise ValueError(f"layout {layout!r}: BNSD or BSND")
-        if len(k.shape) != len(want) or any(w is not None and w != n for w, n in zip(want, k.shape)):
-            raise ValueError(f"k: shape {tuple(k.shape)} does not go with q's {tuple(q.shape)}")
-        if k.dtype != q.dtype:
-            raise TypeError(f"k: {k.dtype}, q: {q.dtype}")
-        if k.device != q.device or not q.is_cuda:
-            raise ValueError(f"q is on {q.device}, k on {k.device}: one CUDA device expected")
-
-    def strides(self, t):
-        """(batch, head, seq) of a tensor of q's or k's dims; dimensions of one
-        element get a stride that passes the checks, whatever torch keeps."""
-        st, n = t.stride(), t.shape
-        if len(n) == 3:
-            st, n = (8,) + st, (1,) + tuple(n)
-        st = [s if m > 1 else 8 for s, m in zip(st, n)]
-        return Strides(st[0], st[1], st[2]) if self.bnsd else Strides(st[0], st[2], st[1])
+def _strides(t, bsnd):
+    """(batch, head, seq) of a tensor of q's or k's dims; dimensions of one element get a stride
+    that passes the checks, whatever torch keeps there."""
+    n = t.shape
+    if len(n) == 3:
+        s, h, _ = t.stride()
+        return 8, (h if n[1] > 1 else 8), (s if n[0] > 1 else 8)
+    b, x, y, _ = t.stride()
+    b = b if n[0] > 1 else 8
+    x = x if n[1] > 1 else 8
+    y = y if n[2] > 1 else 8
+    return (b, y, x) if bsnd else (b, x, y)
 
 
 def _usable(t):
-    """t, or a dense copy where its strides (a transposed or expanded view, an odd
-    offset) are none that the kernels take."""
-    st, n = t.stride(), t.shape
-    fine = st[-1] == 1 and t.data_ptr() % 16 == 0
-    for s, m in zip(st[:-1], n[:-1]):
-        fine = fine and (m <= 1 or (s > 0 and s % 8 == 0))
-    return t if fine else t.clone(memory_format=torch.contiguous_format)
+    """t, or a dense copy where its strides (a transposed or expanded view, an odd offset) are
+    none that the kernels take."""
+    if t.data_ptr() % 16 == 0 and t.stride(-1) == 1:
+        if t.is_contiguous():
+            return t
+        for s, n in zip(t.stride()[:-1], t.shape):
+            if n > 1 and (s <= 0 or s % 8 != 0):
+                break
+        else:
+            return t
+    return t.clone(memory_format=torch.contiguous_format)
 
 
-def _positions(positions, inv_freq, pair_axis, sh, packed, dev):
+def _positions(positions, inv_freq, pair_axis, B, S, packed, index):
     """(positions [n_axes, B, S] or None, n_axes, rot_dim, pair_axis as bytes or None)."""
     if inv_freq is None:
         return None, 1, 0, None
-    _check("inv_freq", inv_freq, torch.float64, (None,), dev)
+    if inv_freq.dtype is not _F64 or inv_freq.dim() != 1 or inv_freq.get_device() != index or not inv_freq.is_contiguous():
+        _check("inv_freq", inv_freq, _F64, (None,), index)
     rot = 2 * inv_freq.shape[0]
     if positions is None:
         raise ValueError("a rotation (inv_freq) needs positions")
-    if positions.dtype != torch.int32:
-        raise TypeError(f"positions: {positions.dtype}, expected {torch.int32}")
-    if positions.device != dev:
-        raise ValueError(f"positions are on {positions.device}, expected {dev}")
-    axes, dims, n = 1, positions.dim(), tuple(positions.shape)
-    if dims == 3 or (packed and dims == 2):
-        axes = n[0]
-    want = ((sh.S,), (axes, sh.S)) if packed else ((sh.S,), (sh.B, sh.S), (axes, sh.B, sh.S))
-    if n not in want:
-        raise ValueError(f"positions: shape {n} does not go with {sh.B} x {sh.S} tokens")
-    if dims == 1 and sh.B > 1:
-        positions = positions.expand(sh.B, sh.S)
+    if positions.dtype is not _I32:
+        raise TypeError(f"positions: {positions.dtype}, expected {_I32}")
+    if positions.get_device() != index:
+        raise ValueError(f"positions are on {positions.device}, expected cuda:{index}")
+    n = positions.shape
+    dims = len(n)
+    axes = n[0] if dims == 3 or (packed and dims == 2) else 1
+    if n != (S,) and (n != (axes, S) if packed else n != (B, S) and n != (axes, B, S)):
+        raise ValueError(f"positions: shape {tuple(n)} does not go with {B} x {S} tokens")
+    if dims == 1 and B > 1:
+        positions = positions.expand(B, S)
     if not positions.is_contiguous():
         positions = positions.contiguous()
     if pair_axis is not None:
@@ -81,38 +95,41 @@ def _positions(positions, inv_freq, pair_axis, sh, packed, dev):
     return positions, axes, rot, pair_axis
 
 
-def _weights(q_weight, k_weight, sh, dtype, dev):
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _check(name, w, dtype, (sh.D,), dev)
+def _weight(name, w, D, dtype, index):
+    """A weight's address (None for none)."""
+    if w is None:
+        return None
+    if not _is(w, dtype, (D,), index):
+        _check(name, w, dtype, (D,), index)
+    return w.data_ptr()
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_four_strides = struct.Struct("12q").pack
+_six_strides = struct.Struct("18q").pack
+
+
 def _forward(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, pair_axis, interleaved, layout, out):
     dt = _dtype_of("q", q)
-    sh = _Shape(q, k, layout)
-    dev = q.device
-    pos, axes, rot, axis = _positions(positions, inv_freq, pair_axis, sh, q.dim() == 3, dev)
-    _weights(q_weight, k_weight, sh, q.dtype, dev)
+    B, S, H, H_kv, D, bsnd = _sizes(q, k, layout)
+    index = q.get_device()
+    pos, axes, rot, axis = _positions(positions, inv_freq, pair_axis, B, S, q.dim() == 3, index)
+    wq = _weight("q_weight", q_weight, D, q.dtype, index)
+    wk = _weight("k_weight", k_weight, D, q.dtype, index)
     q, k = _usable(q), _usable(k)
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=dev), torch.empty(k.shape, dtype=q.dtype, device=dev))
+        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device), torch.empty(k.shape, dtype=q.dtype, device=q.device))
     else:
         for name, t, x in (("out[0]", out[0], q), ("out[1]", out[1], k)):
-            if t.dtype != x.dtype or t.shape != x.shape or t.device != dev or t.stride(-1) != 1:
-                raise ValueError(f"{name}: expected {tuple(x.shape)} of {x.dtype} on {dev}, the head dimension contiguous")
-    strides = (Strides * 4)(sh.strides(q), sh.strides(k), sh.strides(out[0]), sh.strides(out[1]))
-    with _on(dev):
-        st = load().fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
-                                    _ptr(q_weight), _ptr(k_weight), _ptr(pos), _ptr(inv_freq), sh.B, sh.S,
-                                    sh.H, sh.H_kv, sh.D, rot, axes, axis, int(bool(interleaved)),
-                                    int(bool(norm)), eps, strides, dt,
-                                    torch.cuda.current_stream(dev).cuda_stream)
-    if st != 0:
-        raise FaError(st, "fa_qk_norm_rope")
+            if t.dtype is not x.dtype or t.shape != x.shape or t.get_device() != index or t.stride(-1) != 1:
+                raise ValueError(f"{name}: expected {tuple(x.shape)} of {x.dtype} on {x.device}, the head dimension contiguous")
+    strides = _four_strides(*_strides(q, bsnd), *_strides(k, bsnd), *_strides(out[0], bsnd), *_strides(out[1], bsnd))
+    _call("fa_qk_norm_rope", load().fa_qk_norm_rope, index, q.data_ptr(), k.data_ptr(), out[0].data_ptr(),
+          out[1].data_ptr(), wq, wk, _ptr(pos), _ptr(inv_freq), B, S, H, H_kv, D, rot, axes, axis,
+          1 if interleaved else 0, 1 if norm else 0, eps, strides, dt)
     return out
 
 
@@ -123,34 +140,30 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
     outputs and its inputs.  A weight's gradient is None where the forward had no
     such weight, or with weight_grads=False."""
     dt = _dtype_of("q", q)
-    sh = _Shape(q, k, layout)
-    dev = q.device
-    pos, axes, rot, axis = _positions(positions, inv_freq, pair_axis, sh, q.dim() == 3, dev)
-    _weights(q_weight, k_weight, sh, q.dtype, dev)
+    B, S, H, H_kv, D, bsnd = _sizes(q, k, layout)
+    index = q.get_device()
+    pos, axes, rot, axis = _positions(positions, inv_freq, pair_axis, B, S, q.dim() == 3, index)
+    wq = _weight("q_weight", q_weight, D, q.dtype, index)
+    wk = _weight("k_weight", k_weight, D, q.dtype, index)
     for name, t, x in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
-        if t.dtype != x.dtype or t.shape != x.shape or t.device != dev:
-            raise ValueError(f"{name}: expected {tuple(x.shape)} of {x.dtype} on {dev}")
+        if t.dtype is not x.dtype or t.shape != x.shape or t.get_device() != index:
+            raise ValueError(f"{name}: expected {tuple(x.shape)} of {x.dtype} on {x.device}")
     dq_out, dk_out, q, k = _usable(dq_out), _usable(dk_out), _usable(q), _usable(k)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    dqw = torch.empty_like(q_weight) if q_weight is not None and weight_grads else None
-    dkw = torch.empty_like(k_weight) if k_weight is not None and weight_grads else None
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    dqw = torch.empty_like(q_weight) if weight_grads and q_weight is not None else None
+    dkw = torch.empty_like(k_weight) if weight_grads and k_weight is not None else None
     ws, nbytes = None, 0
     if dqw is not None or dkw is not None:
-        st, nbytes = fa_qk_norm_rope_bwd_workspace_size(sh.D)
+        st, nbytes = fa_qk_norm_rope_bwd_workspace_size(D)
         if st != 0:
             raise FaError(st, "fa_qk_norm_rope_bwd_workspace_size")
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    strides = (Strides * 6)(*(sh.strides(t) for t in (dq_out, dk_out, q, k, dq, dk)))
-    with _on(dev):
-        st = load().fa_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(),
-                                        dq.data_ptr(), dk.data_ptr(), _ptr(q_weight), _ptr(k_weight),
-                                        _ptr(dqw), _ptr(dkw), _ptr(pos), _ptr(inv_freq), sh.B, sh.S, sh.H,
-                                        sh.H_kv, sh.D, rot, axes, axis, int(bool(interleaved)),
-                                        int(bool(norm)), eps, strides, dt, _ptr(ws), nbytes,
-                                        torch.cuda.current_stream(dev).cuda_stream)
-    if st != 0:
-        raise FaError(st, "fa_qk_norm_rope_bwd")
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    strides = _six_strides(*_strides(dq_out, bsnd), *_strides(dk_out, bsnd), *_strides(q, bsnd), *_strides(k, bsnd),
+                           *_strides(dq, bsnd), *_strides(dk, bsnd))
+    _call("fa_qk_norm_rope_bwd", load().fa_qk_norm_rope_bwd, index, dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(),
+          k.data_ptr(), dq.data_ptr(), dk.data_ptr(), wq, wk, _ptr(dqw), _ptr(dkw), _ptr(pos), _ptr(inv_freq), B, S, H,
+          H_kv, D, rot, axes, axis, 1 if interleaved else 0, 1 if norm else 0, eps, strides, dt, _ptr(ws), nbytes)
     return dq, dk, dqw, dkw
 
 
