@@ -2,19 +2,18 @@
  * fa_kv4.cu -- fa_kv4_write and fa_kv4_read: rows of keys and values into and
  * out of the 4-bit cache (formulas in include/fa_api.h).
  *
- * Bound by HBM (2 bytes a value one way, 9/16 the other).  A thread takes one
- * group of 16 values: two 16-byte accesses to the 16-bit row, one of 8 bytes
- * to the codes and one byte of scale; consecutive threads take consecutive
- * groups, so a warp's accesses are contiguous on the 16-bit side and fall into
- * whole rows on the cache's.
+ * Bound by HBM (2 bytes a value one way, 9/16 the other).  Writing, a thread
+ * takes one group of 16 values: two 16-byte loads, one store of 8 bytes of codes
+ * and one byte of scale, so that the codes fall into whole rows.  Reading, it
+ * takes 8 values a time, so that each store of a warp fills whole lines.
  *
  * The nearest code is decided exactly.  16-bit inputs lie on a border between
  * two codes (or two scales) often, and one rounding of x / (scale * descale)
  * in fp32 would settle those by its own error.  So the fp32 quotient is only
- * a first guess, cut to 11 bits: every border has fewer bits, so the guess is
+ * a first guess, cut to a few bits: every border has fewer, so the guess is
  * either on the right side of it or the border itself, and then the sign of
  * the remainder x - guess * scale * descale, which one fma gives exactly,
- * moves it off the border by a bit.
+ * moves it a little off the border.
  */
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,16 +37,27 @@ struct RowParams {
   void* out[2];            // read: K, V rows
   int64_t token_stride[2], head_stride[2];   // elements (write)
   const int64_t* slot_map;
-  int64_t n_groups;        // n_tokens * H_kv * D / 16
+  int64_t n_tokens, n_groups;   // groups: n_tokens * H_kv * D / 16
+  int32_t tile;            // read: tokens of a block
   int64_t n_slots;
 };
 
-// q = num / (f * g) up to 2^-22, as a float whose place among numbers of at
-// most 10 bits is that of the exact quotient; f has at most 4 bits.
-__device__ __forceinline__ float place(float q, float f, float g, float num) {
+// amax / (6 g) for the scale: q is that up to 2^-22; the result's place among
+// numbers of at most 10 bits is that of the exact quotient.
+__device__ __forceinline__ float place_scale(float q, float g, float amax) {
   const uint32_t h = (__float_as_uint(q) + 0x1000u) & 0xffffe000u;
-  const float rest = fmaf(-(__uint_as_float(h) * f), g, num);
+  const float rest = fmaf(-(__uint_as_float(h) * 6.0f), g, amax);
   return __uint_as_float(h + (rest > 0.0f ? 1u : 0u) - (rest < 0.0f ? 1u : 0u));
+}
+// a / (scale g) in [0, 8] for a code, likewise: the borders are multiples of
+// 1/4, so the guess is cut to multiples of 2^-6 (by adding and taking away 2^17
+// and a half) and moved off by 2^-8.
+__device__ __forceinline__ float place_code(float q, float scale, float g, float a) {
+  const float h = (q + 196608.0f) - 196608.0f;
+  const float rest = fmaf(-(h * scale), g, a);
+  float side;                                     // 0, 1/2 or 1: below, on, above
+  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(side) : "f"(rest), "f"(8.507059173023462e37f), "f"(0.5f));
+  return fmaf(side, 0.0078125f, h - 0.00390625f);
 }
 
 // Where a group lives: its token, head and group within the row.
@@ -77,16 +87,6 @@ template <> __device__ __forceinline__ float2 unpack<__half>(uint32_t w) {
 template <> __device__ __forceinline__ float2 unpack<__nv_bfloat16>(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-template <typename T> __device__ __forceinline__ uint32_t pack(float a, float b);
-template <> __device__ __forceinline__ uint32_t pack<__half>(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <> __device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const __grid_constant__ RowParams p) {
   fa::wait_for_stream();
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const __grid_con
     amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));   // fmaxf passes NaN over
   }
   const float g = p.cache.descale[which];
-  const float want = place(fminf(amax * __frcp_rn(6.0f * g), 1024.0f), 6.0f, g, amax);
+  const float want = place_scale(fminf(amax * __frcp_rn(6.0f * g), 1024.0f), g, amax);
   uint16_t code;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(code) : "f"(0.0f), "f"(want));
   const uint32_t h2 = fa::kv4::scales_to_half(code);
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const __grid_con
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const float a = fabsf(x[j]);
-      y[j] = copysignf(place(fminf(a * inv, 8.0f), scale, g, a), x[j]);   // fminf: NaN becomes 8
+      y[j] = copysignf(place_code(fminf(a * inv, 8.0f), scale, g, a), x[j]);   // fminf: NaN becomes 8
     }
     uint32_t w[2];
 #pragma unroll
@@ -139,35 +139,21 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const __grid_con
   p.cache.scales[which][row * (D / 16) + at.g] = static_cast<uint8_t>(code);
 }
 
+// A block reads `tile` tokens (at most 32) of K or of V.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) fa_kv4_read_kernel(const __grid_constant__ RowParams p) {
+  __shared__ int64_t row[32];
   fa::wait_for_stream();
-  const int which = blockIdx.y;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= p.n_groups) return;
-  const Group<D> at(i, p.cache.H_kv);
-  const int64_t slot = p.slot_map[at.token];
-  uint32_t w[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = 0u;
-  if (slot >= 0 && slot < p.n_slots) {
-    const int64_t row = cache_row(p.cache, slot, at.head);
-    const uint2 codes = *reinterpret_cast<const uint2*>(p.cache.codes[which] + row * (D / 2) + at.g * 8);
-    const uint32_t s = p.cache.scales[which][row * (D / 16) + at.g];
-    const uint32_t s2 = fa::kv4::scales_to_half(s | (s << 8));
-    const float g = p.cache.descale[which];
-    uint32_t h[2][4];
-    fa::kv4::codes_to_half(codes.x, h[0]);
-    fa::kv4::codes_to_half(codes.y, h[1]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 v = unpack<__half>(fa::kv4::mul_half(h[j / 4][j % 4], s2));
-      w[j] = pack<T>(v.x * g, v.y * g);
-    }
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * p.tile;
+  const int n = static_cast<int>(min(static_cast<int64_t>(p.tile), p.n_tokens - first));
+  if (threadIdx.x < n) {
+    const int64_t slot = p.slot_map[first + threadIdx.x];
+    row[threadIdx.x] = slot >= 0 && slot < p.n_slots ? cache_row(p.cache, slot, 0) : -1;
   }
-  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[which]) + i * 16);
-  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  __syncthreads();
+  const int which = blockIdx.y;
+  fa::kv4::unpack_rows<T, D, kThreads>(p.cache, which, row, n,
+                                       static_cast<uint16_t*>(p.out[which]) + first * p.cache.H_kv * D);
 }
 
 bool off(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
@@ -204,14 +190,15 @@ RowParams params(const uint8_t* kc, const uint8_t* ks, const uint8_t* vc, const 
   p.cache.page_size = static_cast<int32_t>(page_size);
   p.cache.H_kv = static_cast<int32_t>(H_kv);
   p.slot_map = slot_map;
+  p.n_tokens = n_tokens;
   p.n_groups = n_tokens * H_kv * (D / 16);
   p.n_slots = num_pages * page_size;
   return p;
 }
 
 template <typename K>
-fa_status_t launch(K kernel, const RowParams& p, cudaStream_t stream) {
-  const fa::Launch c(dim3(static_cast<unsigned>((p.n_groups + kThreads - 1) / kThreads), 2), kThreads, 0, stream);
+fa_status_t launch(K kernel, const RowParams& p, int64_t blocks, cudaStream_t stream) {
+  const fa::Launch c(dim3(static_cast<unsigned>(blocks), 2), kThreads, 0, stream);
   return cudaLaunchKernelEx(&c.cfg, kernel, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -239,11 +226,12 @@ fa_status_t fa_kv4_write(const void* k, const void* v, const int64_t* slot_map, 
                        n_tokens, H_kv, D, page_size, num_pages);
   p.in[0] = k; p.in[1] = v;
   for (int i = 0; i < 2; ++i) { p.token_stride[i] = strides[i].seq; p.head_stride[i] = strides[i].head; }
+  const int64_t blocks = (p.n_groups + kThreads - 1) / kThreads;
   if (dtype == FA_DTYPE_F16)
-    return D == 64 ? launch(fa_kv4_write_kernel<__half, 64>, p, stream)
-                   : launch(fa_kv4_write_kernel<__half, 128>, p, stream);
-  return D == 64 ? launch(fa_kv4_write_kernel<__nv_bfloat16, 64>, p, stream)
-                 : launch(fa_kv4_write_kernel<__nv_bfloat16, 128>, p, stream);
+    return D == 64 ? launch(fa_kv4_write_kernel<__half, 64>, p, blocks, stream)
+                   : launch(fa_kv4_write_kernel<__half, 128>, p, blocks, stream);
+  return D == 64 ? launch(fa_kv4_write_kernel<__nv_bfloat16, 64>, p, blocks, stream)
+                 : launch(fa_kv4_write_kernel<__nv_bfloat16, 128>, p, blocks, stream);
 }
 
 fa_status_t fa_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
@@ -258,11 +246,15 @@ fa_status_t fa_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales, const u
   RowParams p = params(k_codes, k_scales, v_codes, v_scales, descale_k, descale_v, slot_map,
                        n_tokens, H_kv, D, page_size, num_pages);
   p.out[0] = k_out; p.out[1] = v_out;
+  // 32 tokens a block, or fewer while that leaves SMs idle
+  p.tile = 32;
+  while (p.tile > 1 && n_tokens < int64_t(p.tile) * 152 * 2) p.tile /= 2;
+  const int64_t blocks = (n_tokens + p.tile - 1) / p.tile;
   if (dtype == FA_DTYPE_F16)
-    return D == 64 ? launch(fa_kv4_read_kernel<__half, 64>, p, stream)
-                   : launch(fa_kv4_read_kernel<__half, 128>, p, stream);
-  return D == 64 ? launch(fa_kv4_read_kernel<__nv_bfloat16, 64>, p, stream)
-                 : launch(fa_kv4_read_kernel<__nv_bfloat16, 128>, p, stream);
+    return D == 64 ? launch(fa_kv4_read_kernel<__half, 64>, p, blocks, stream)
+                   : launch(fa_kv4_read_kernel<__half, 128>, p, blocks, stream);
+  return D == 64 ? launch(fa_kv4_read_kernel<__nv_bfloat16, 64>, p, blocks, stream)
+                 : launch(fa_kv4_read_kernel<__nv_bfloat16, 128>, p, blocks, stream);
 }
 
 }  // extern "C"

@@ -3,6 +3,7 @@
  * of its codes (include/fa_api.h states the format).
  */
 #pragma once
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -37,6 +38,68 @@ __device__ __forceinline__ uint32_t scales_to_half(uint32_t two) {
 __device__ __forceinline__ uint32_t mul_half(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+template <typename T> __device__ __forceinline__ uint32_t pack16(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack16<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Rows of the cache as dense 16-bit rows out[r][head][D], r < n <= 32, by a block
+// of THREADS: row[r] is the index (page, head 0, row of the page) of token r in
+// the cache, negative for a row of zeros.  A thread unpacks 8 values at a time
+// (4 bytes of codes, one store of 16); consecutive threads take consecutive
+// pieces of the output, so the stores fill whole lines.
+template <typename T, int D, int THREADS>
+__device__ __forceinline__ void unpack_rows(const Cache& c, int which, const int64_t* row, int n, void* out) {
+  constexpr int P = D / 8, kAhead = 4;              // pieces of a head; pieces in flight
+  constexpr int R = THREADS / P;                    // (token, head) rows the block takes at once
+  const int piece = threadIdx.x % P;
+  const int h_step = R % c.H_kv, t_step = R / c.H_kv;
+  int t = threadIdx.x / P / c.H_kv, h = threadIdx.x / P % c.H_kv;
+  const float g = c.descale[which];
+  uint4* dst = reinterpret_cast<uint4*>(out) + threadIdx.x;
+  while (t < n) {
+    uint32_t codes[kAhead], scale[kAhead];
+    int last = 0;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      codes[k] = scale[k] = 0u;
+      if (t < n) {
+        last = k + 1;
+        const int64_t at = row[t];
+        if (at >= 0) {
+          const uint64_t r = static_cast<uint64_t>(at) + static_cast<uint32_t>(h) * static_cast<uint32_t>(c.page_size);
+          codes[k] = *reinterpret_cast<const uint32_t*>(c.codes[which] + r * (D / 2) + piece * 4);
+          scale[k] = c.scales[which][r * (D / 16) + piece / 2];
+        }
+      }
+      t += t_step;
+      h += h_step;
+      if (h >= c.H_kv) { h -= c.H_kv; ++t; }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (k < last) {
+        uint32_t v[4], w[4];
+        codes_to_half(codes[k], v);
+        const uint32_t s2 = scales_to_half(scale[k] * 0x101u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x = mul_half(v[j], s2);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+          w[j] = pack16<T>(f.x * g, f.y * g);
+        }
+        dst[static_cast<int64_t>(k) * THREADS] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    dst += static_cast<int64_t>(kAhead) * THREADS;
+  }
 }
 
 // The paged attention's page sizes: tiles of 16 keys lie in one page.

@@ -868,7 +868,6 @@ __global__ void __launch_bounds__(kUnpackThreads) fa_kv4_unpack_kernel(const __g
 
   // and zeros behind the last sequence, where its last tile of 128 keys ends
   const int64_t used = cu[n], rows = min(used + 128, p.total_k);
-  const int groups = p.cache.H_kv * (D / 16);
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * kUnpackRows; base < rows;
        base += static_cast<int64_t>(gridDim.x) * kUnpackRows) {
     __syncthreads();
@@ -890,38 +889,10 @@ __global__ void __launch_bounds__(kUnpackThreads) fa_kv4_unpack_kernel(const __g
       where[tid] = row;
     }
     __syncthreads();
-    const int todo = static_cast<int>(min(static_cast<int64_t>(kUnpackRows), rows - base));
     const int which = blockIdx.y;
-    for (int i = tid; i < todo * groups; i += kUnpackThreads) {
-      const int r = i / groups, rest = i - r * groups, head = rest / (D / 16), gr = rest % (D / 16);
-      uint32_t w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = 0u;
-      if (where[r] >= 0) {
-        const int64_t row = where[r] + static_cast<int64_t>(head) * p.cache.page_size;
-        const uint2 codes = *reinterpret_cast<const uint2*>(p.cache.codes[which] + row * (D / 2) + gr * 8);
-        const uint32_t s = p.cache.scales[which][row * (D / 16) + gr];
-        const uint32_t s2 = scales_to_half(s | (s << 8));
-        const float dv = p.cache.descale[which];
-        uint32_t h[2][4];
-        codes_to_half(codes.x, h[0]);
-        codes_to_half(codes.y, h[1]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t v = mul_half(h[j / 4][j % 4], s2);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
-          if (std::is_same<T, __half>::value) {
-            w[j] = pack_half(f.x * dv, f.y * dv);
-          } else {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * dv, f.y * dv);
-            w[j] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-        }
-      }
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[which]) + ((base + r) * groups + rest) * 16);
-      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
+    fa::kv4::unpack_rows<T, D, kUnpackThreads>(p.cache, which, where,
+                                               static_cast<int>(min(static_cast<int64_t>(kUnpackRows), rows - base)),
+                                               static_cast<uint16_t*>(p.out[which]) + base * p.cache.H_kv * D);
   }
 }
 

@@ -2,6 +2,7 @@
 tensors (fa_qk_norm_rope and its backward; formulas in include/fa_api.h)."""
 from __future__ import annotations
 
+import functools
 import struct
 
 import torch
@@ -38,32 +39,32 @@ def _sizes(q, k, layout):
     return B, S, H, h_kv, D, bsnd
 
 
-def _strides(t, bsnd):
-    """(batch, head, seq) of a tensor of q's or k's dims; dimensions of one element get a stride
-    that passes the checks, whatever torch keeps there."""
-    n = t.shape
-    if len(n) == 3:
-        s, h, _ = t.stride()
-        return 8, (h if n[1] > 1 else 8), (s if n[0] > 1 else 8)
-    b, x, y, _ = t.stride()
-    b = b if n[0] > 1 else 8
-    x = x if n[1] > 1 else 8
-    y = y if n[2] > 1 else 8
-    return (b, y, x) if bsnd else (b, x, y)
+def _place(t, bsnd):
+    """(t, address, batch, head and seq stride) of a tensor of q's or k's dims; t is a dense copy
+    where the strides (of a transposed or expanded view, an odd offset) are none that the kernels
+    take.  Dimensions of one element get a stride that passes the checks, whatever torch keeps."""
+    ptr, st = t.data_ptr(), t.stride()
+    if len(st) == 4:
+        b, x, y, one = st
+        if one == 1 and not ptr & 15 and not (b | x | y) & 7 and b > 0 and x > 0 and y > 0:
+            return (t, ptr, b, y, x) if bsnd else (t, ptr, b, x, y)
+    fine = st[-1] == 1 and ptr % 16 == 0
+    for s, n in zip(st[:-1], t.shape):
+        fine = fine and (n <= 1 or (s > 0 and s % 8 == 0))
+    if not fine:
+        t = t.clone(memory_format=torch.contiguous_format)
+    st = [s if n > 1 else 8 for s, n in zip(t.stride(), t.shape)]
+    if len(st) == 3:
+        return t, t.data_ptr(), 8, st[1], st[0]
+    return (t, t.data_ptr(), st[0], st[2], st[1]) if bsnd else (t, t.data_ptr(), st[0], st[1], st[2])
 
 
-def _usable(t):
-    """t, or a dense copy where its strides (a transposed or expanded view, an odd offset) are
-    none that the kernels take."""
-    if t.data_ptr() % 16 == 0 and t.stride(-1) == 1:
-        if t.is_contiguous():
-            return t
-        for s, n in zip(t.stride()[:-1], t.shape):
-            if n > 1 and (s <= 0 or s % 8 != 0):
-                break
-        else:
-            return t
-    return t.clone(memory_format=torch.contiguous_format)
+def _new(t, B, S, H, D, bsnd):
+    """_place of a new dense tensor of t's shape."""
+    o = torch.empty_like(t, memory_format=torch.contiguous_format)
+    if bsnd:
+        return o, o.data_ptr(), S * H * D or 8, D, H * D
+    return o, o.data_ptr(), S * H * D or 8, S * D or 8, D
 
 
 def _positions(positions, inv_freq, pair_axis, B, S, packed, index):
@@ -119,18 +120,32 @@ def _forward(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, pair_axis
     pos, axes, rot, axis = _positions(positions, inv_freq, pair_axis, B, S, q.dim() == 3, index)
     wq = _weight("q_weight", q_weight, D, q.dtype, index)
     wk = _weight("k_weight", k_weight, D, q.dtype, index)
-    q, k = _usable(q), _usable(k)
+    q, qp, *qs = _place(q, bsnd)
+    k, kp, *ks = _place(k, bsnd)
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device), torch.empty(k.shape, dtype=q.dtype, device=q.device))
+        qo, qop, *qos = _new(q, B, S, H, D, bsnd)
+        ko, kop, *kos = _new(k, B, S, H_kv, D, bsnd)
+        out = qo, ko
     else:
         for name, t, x in (("out[0]", out[0], q), ("out[1]", out[1], k)):
             if t.dtype is not x.dtype or t.shape != x.shape or t.get_device() != index or t.stride(-1) != 1:
                 raise ValueError(f"{name}: expected {tuple(x.shape)} of {x.dtype} on {x.device}, the head dimension contiguous")
-    strides = _four_strides(*_strides(q, bsnd), *_strides(k, bsnd), *_strides(out[0], bsnd), *_strides(out[1], bsnd))
-    _call("fa_qk_norm_rope", load().fa_qk_norm_rope, index, q.data_ptr(), k.data_ptr(), out[0].data_ptr(),
-          out[1].data_ptr(), wq, wk, _ptr(pos), _ptr(inv_freq), B, S, H, H_kv, D, rot, axes, axis,
-          1 if interleaved else 0, 1 if norm else 0, eps, strides, dt)
+        qo, qop, *qos = _place(out[0], bsnd)
+        ko, kop, *kos = _place(out[1], bsnd)
+        if qo is not out[0] or ko is not out[1]:
+            raise ValueError("out: strides and addresses have to be positive multiples of 16 bytes")
+    _call("fa_qk_norm_rope", load().fa_qk_norm_rope, index, qp, kp, qop, kop, wq, wk, _ptr(pos), _ptr(inv_freq), B, S,
+          H, H_kv, D, rot, axes, axis, 1 if interleaved else 0, 1 if norm else 0, eps,
+          _four_strides(*qs, *ks, *qos, *kos), dt)
     return out
+
+
+@functools.lru_cache(None)
+def _workspace_bytes(D):
+    st, nbytes = fa_qk_norm_rope_bwd_workspace_size(D)
+    if st != 0:
+        raise FaError(st, "fa_qk_norm_rope_bwd_workspace_size")
+    return nbytes
 
 
 def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight=None, k_weight=None,
@@ -148,22 +163,21 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
     for name, t, x in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
         if t.dtype is not x.dtype or t.shape != x.shape or t.get_device() != index:
             raise ValueError(f"{name}: expected {tuple(x.shape)} of {x.dtype} on {x.device}")
-    dq_out, dk_out, q, k = _usable(dq_out), _usable(dk_out), _usable(q), _usable(k)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    dq_out, gqp, *gqs = _place(dq_out, bsnd)
+    dk_out, gkp, *gks = _place(dk_out, bsnd)
+    q, qp, *qs = _place(q, bsnd)
+    k, kp, *ks = _place(k, bsnd)
+    dq, dqp, *dqs = _new(q, B, S, H, D, bsnd)
+    dk, dkp, *dks = _new(k, B, S, H_kv, D, bsnd)
     dqw = torch.empty_like(q_weight) if weight_grads and q_weight is not None else None
     dkw = torch.empty_like(k_weight) if weight_grads and k_weight is not None else None
     ws, nbytes = None, 0
     if dqw is not None or dkw is not None:
-        st, nbytes = fa_qk_norm_rope_bwd_workspace_size(D)
-        if st != 0:
-            raise FaError(st, "fa_qk_norm_rope_bwd_workspace_size")
+        nbytes = _workspace_bytes(D)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    strides = _six_strides(*_strides(dq_out, bsnd), *_strides(dk_out, bsnd), *_strides(q, bsnd), *_strides(k, bsnd),
-                           *_strides(dq, bsnd), *_strides(dk, bsnd))
-    _call("fa_qk_norm_rope_bwd", load().fa_qk_norm_rope_bwd, index, dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(),
-          k.data_ptr(), dq.data_ptr(), dk.data_ptr(), wq, wk, _ptr(dqw), _ptr(dkw), _ptr(pos), _ptr(inv_freq), B, S, H,
-          H_kv, D, rot, axes, axis, 1 if interleaved else 0, 1 if norm else 0, eps, strides, dt, _ptr(ws), nbytes)
+    _call("fa_qk_norm_rope_bwd", load().fa_qk_norm_rope_bwd, index, gqp, gkp, qp, kp, dqp, dkp, wq, wk, _ptr(dqw),
+          _ptr(dkw), _ptr(pos), _ptr(inv_freq), B, S, H, H_kv, D, rot, axes, axis, 1 if interleaved else 0,
+          1 if norm else 0, eps, _six_strides(*gqs, *gks, *qs, *ks, *dqs, *dks), dt, _ptr(ws), nbytes)
     return dq, dk, dqw, dkw
 
 
