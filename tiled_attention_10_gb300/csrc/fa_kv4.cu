@@ -90,6 +90,7 @@ template <> __device__ __forceinline__ float2 unpack<__nv_bfloat16>(uint32_t w) 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const __grid_constant__ RowParams p) {
   fa::wait_for_stream();
+  fa::let_next_start();
   const int which = blockIdx.y;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   if (i >= p.n_groups) return;
@@ -144,6 +145,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) fa_kv4_read_kernel(const __grid_constant__ RowParams p) {
   __shared__ int64_t row[32];
   fa::wait_for_stream();
+  fa::let_next_start();
   const int64_t first = static_cast<int64_t>(blockIdx.x) * p.tile;
   const int n = static_cast<int>(min(static_cast<int64_t>(p.tile), p.n_tokens - first));
   if (threadIdx.x < n) {

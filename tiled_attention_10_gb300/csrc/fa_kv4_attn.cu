@@ -57,8 +57,8 @@ using fa::kv4::scales_to_half;
 
 constexpr int kStep = 32;           // keys of a warp's step
 constexpr int kChunk = 64;          // keys of a unit of work
-constexpr int kUnitCost = 8;        // chunks that a unit costs beside its own, for an even split
-constexpr int kMinShare = kUnitCost + 4;   // least work of a block, in chunks: any run longer than
+constexpr int kUnitCost = 6;        // chunks that a unit costs beside its own, for an even split
+constexpr int kMinShare = kUnitCost + 1;   // least work of a block, in chunks: any run longer than
                                     // kUnitCost holds keys
 constexpr int kMaxSms = 160;
 constexpr float kBias = 8.0f;       // P is held as 2^(score - max + kBias): small
@@ -247,10 +247,13 @@ __device__ __forceinline__ void load_step(const AttnParams& p, const Lane& me, u
 template <int D, int NT>
 struct Cfg {
   static constexpr int kRows = 8 * NT;
-  // Warps of a block and resident blocks an SM: 16 warps of 128 registers with
-  // 8 rows, 12 of 168 with 16, 8 of 255 with 32 (O and the ring grow).
-  static constexpr int kWarps = NT == 1 ? 8 : 4;
-  static constexpr int kBlocks = NT == 2 ? 3 : 2;
+  // Warps of a block and resident blocks an SM: 12 warps of 168 registers with 8
+  // or 16 rows, 8 of 255 with 32 (O and the ring grow).  With 8 rows, 128
+  // sequences of 8192 keys (floor 178 us): 4 blocks of 3 warps 210 us, 2 x 8
+  // (128 registers) 214, 6 x 2 211, 2 x 4 224; 4000 of 256 keys, where units
+  // end often: 383, 557, 354, 525; one of 65536: 28, 26, 32, 27.
+  static constexpr int kWarps = NT == 1 ? 3 : 4;
+  static constexpr int kBlocks = NT == 1 ? 4 : NT == 2 ? 3 : 2;
   // A warp's ring: three stages; at the end of a unit its O lies in the third
   // one's place (and behind it), while the next unit's first two steps are
   // already on their way to the other two.
@@ -272,9 +275,25 @@ struct Unit {
   int32_t more;                     // another unit of this block follows
 };
 
-// Where a block is in its run of chunks (kept by its first thread).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {   // both >= 0
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// An even split of the work: the first `extra` blocks have share + 1 places.
+struct Split {
+  int64_t share, extra;
+  __device__ __forceinline__ int64_t start(int64_t block) const { return share * block + min(block, extra); }
+  __device__ __forceinline__ int64_t block_of(int64_t place) const {
+    const int64_t edge = extra * (share + 1);
+    return place < edge ? divide(place, share + 1) : extra + divide(place - edge, share);
+  }
+};
+
+// Where a block is in its run of chunks.
 struct Cursor {
-  int64_t w, w1, off, total, blocks;   // next place, end; offset in the sequence; of the launch
+  int64_t w, w1, off;       // next place, end; offset in the sequence
+  Split split;
   int32_t s;
   Seq sq;
 };
@@ -292,13 +311,13 @@ __device__ __noinline__ void next_unit(const AttnParams& p, Cursor& c, Unit& u) 
   // A unit is kUnitCost places without keys and then its chunks; this block's
   // run covers its places [pos, end).
   const int size = sq.chunks + kUnitCost;
-  const int64_t unit = c.off / size;
+  const int64_t unit = divide(c.off, size);
   const int pos = static_cast<int>(c.off - unit * size);
   const int end = static_cast<int>(min(static_cast<int64_t>(size), pos + (c.w1 - c.w)));
   const int c0 = max(pos - kUnitCost, 0), c1 = end - kUnitCost;
   u.q_row0 = sq.q_row0;
   u.s = c.s;
-  u.head = static_cast<int>(unit / sq.tiles);
+  u.head = static_cast<int>(divide(unit, sq.tiles));
   u.row0 = static_cast<int>(unit - static_cast<int64_t>(u.head) * sq.tiles) * ROWS;
   u.rows = static_cast<int>(min(static_cast<int64_t>(ROWS), static_cast<int64_t>(sq.q_len) * p.G - u.row0));
   u.key_begin = c0 * kChunk;
@@ -310,7 +329,7 @@ __device__ __noinline__ void next_unit(const AttnParams& p, Cursor& c, Unit& u) 
   u.piece = c0 > 0 ? 0 : c1 < sq.chunks ? 1 : -1;
   u.pieces = 0;
   if (u.piece == 1)   // up to the block that holds the unit's last chunk
-    u.pieces = static_cast<int32_t>(((c.w - pos + size) * c.blocks - 1) / c.total - blockIdx.x + 1);
+    u.pieces = static_cast<int32_t>(c.split.block_of(c.w - pos + size - 1) - blockIdx.x + 1);
   c.w += end - pos;
   c.off += end - pos;
   u.more = c.w1 - c.w > kUnitCost;    // (what is left begins with a unit: has it keys?)
@@ -333,6 +352,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, Cfg<D, NT>::kBlocks)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   fa::wait_for_stream();
+  fa::let_next_start();
 
   // ---- this block's run of the work and the sequence it starts in
   {
@@ -358,11 +378,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, Cfg<D, NT>::kBlocks)
       if (w < warp) before += scan[w];
       total += scan[w];
     }
-    const int64_t blocks = total == 0 ? 0 : min(static_cast<int64_t>(gridDim.x), max(total / kMinShare, int64_t(1)));
+    const int64_t blocks = total == 0 ? 0 : min(static_cast<int64_t>(gridDim.x), max(divide(total, kMinShare), int64_t(1)));
     const int64_t bid = blockIdx.x;
     if (tid == 0) p.meta[bid].pieces = 0;
     if (bid >= blocks) return;
-    const int64_t w = total * bid / blocks;
+    const int64_t share = divide(total, blocks);
+    const Split split{share, total - share * blocks};
+    const int64_t w = split.start(bid);
     if (w >= before && w < before + mine) {   // one thread has the sequence
       int64_t off = w - before;
       int s = s0;
@@ -374,7 +396,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, Cfg<D, NT>::kBlocks)
           off -= c;
         }
       }
-      cursor = Cursor{w, total * (bid + 1) / blocks, off, total, blocks, s, sq};
+      cursor = Cursor{w, split.start(bid + 1), off, split, s, sq};
       next_unit<kRows>(p, cursor, units[0]);
       if (units[0].more) next_unit<kRows>(p, cursor, units[1]);
     }
@@ -490,7 +512,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, Cfg<D, NT>::kBlocks)
     // kept in registers: not to be read from shared memory again at every step
     asm volatile("" : "+r"(key_begin), "+r"(key_end), "+r"(head));
     // one warp looks for the unit after the next (known to all at the next one)
-    if (lane == 0 && warp == (turn & (kWarps - 1)) && un.more && units[(turn + 1) & 3].more)
+    if (lane == 0 && warp == (turn % kWarps) && un.more && units[(turn + 1) & 3].more)
       next_unit<kRows>(p, cursor, units[(turn + 2) & 3]);
     __syncwarp();
     // this lane's accumulators are rows 8 j + 2 t and 8 j + 2 t + 1
@@ -754,6 +776,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_kv4_merge_kernel(const __
   constexpr int E = D / 32;              // elements a lane
   __shared__ float sum_o[kMergeWarps][D], sum_w[kMergeWarps];
   fa::wait_for_stream();
+  fa::let_next_start();
   const Meta mt = p.meta[blockIdx.x];
   if (mt.pieces == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -771,7 +794,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_kv4_merge_kernel(const __
       for (int i = lane; i < mt.pieces; i += 32) top = fmaxf(top, p.part_lse[at(i)]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-#pragma unroll 4
+#pragma unroll 8
       for (int i = part; i < mt.pieces; i += share) {
         const int64_t a = at(i);
         const float lse = p.part_lse[a];
@@ -836,9 +859,10 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kUnpackThreads) fa_kv4_unpack_kernel(const __grid_constant__ UnpackParams p) {
   extern __shared__ int32_t cu[];         // [n_seqs + 1] key rows before each sequence
   __shared__ int64_t warp_sum[kUnpackThreads / 32];
-  __shared__ int64_t where[kUnpackRows];  // row (page, 0, row of the page) in the cache, or -1
+  __shared__ int64_t where[2][kUnpackRows];   // row (page, 0, row of the page) in the cache, or -1
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.n_seqs;
   fa::wait_for_stream();
+  fa::let_next_start();
   // keys of a sequence: none where it brings no queries
   auto keys = [&](int s) -> int64_t {
     return p.cu_q[s + 1] > p.cu_q[s] ? min(max(static_cast<int64_t>(p.seqused_k[s]), int64_t(0)), p.max_keys) : 0;
@@ -868,31 +892,36 @@ __global__ void __launch_bounds__(kUnpackThreads) fa_kv4_unpack_kernel(const __g
 
   // and zeros behind the last sequence, where its last tile of 128 keys ends
   const int64_t used = cu[n], rows = min(used + 128, p.total_k);
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kUnpackRows; base < rows;
-       base += static_cast<int64_t>(gridDim.x) * kUnpackRows) {
-    __syncthreads();
-    if (tid < kUnpackRows) {
-      int64_t row = -1;
-      const int64_t i = base + tid;
-      if (i < used) {
-        int lo = 0, hi = n;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (cu[mid] <= i) lo = mid; else hi = mid;
-        }
-        const int key = static_cast<int>(i - cu[lo]), ps = p.cache.page_size;
-        const int col = key / ps;
-        const int page = p.block_table[static_cast<int64_t>(lo) * p.max_pages + col];
-        if (page >= 0 && page < p.cache.num_pages)
-          row = static_cast<int64_t>(page) * p.cache.H_kv * ps + (key - col * ps);
+  // Where a tile's rows are is looked up while the tile before it is unpacked.
+  auto look = [&](int64_t base, int64_t* to) {
+    if (tid >= kUnpackRows) return;
+    int64_t row = -1;
+    const int64_t i = base + tid;
+    if (i < used) {
+      int lo = 0, hi = n;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= i) lo = mid; else hi = mid;
       }
-      where[tid] = row;
+      const int key = static_cast<int>(i - cu[lo]), ps = p.cache.page_size;
+      const int col = key / ps;
+      const int page = p.block_table[static_cast<int64_t>(lo) * p.max_pages + col];
+      if (page >= 0 && page < p.cache.num_pages)
+        row = static_cast<int64_t>(page) * p.cache.H_kv * ps + (key - col * ps);
     }
-    __syncthreads();
-    const int which = blockIdx.y;
-    fa::kv4::unpack_rows<T, D, kUnpackThreads>(p.cache, which, where,
+    to[tid] = row;
+  };
+  const int which = blockIdx.y;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kUnpackRows;
+  int64_t base = static_cast<int64_t>(blockIdx.x) * kUnpackRows;
+  look(base, where[0]);
+  __syncthreads();
+  for (int b = 0; base < rows; base += step, b ^= 1) {
+    look(base + step, where[b ^ 1]);
+    fa::kv4::unpack_rows<T, D, kUnpackThreads>(p.cache, which, where[b],
                                                static_cast<int>(min(static_cast<int64_t>(kUnpackRows), rows - base)),
                                                static_cast<uint16_t*>(p.out[which]) + base * p.cache.H_kv * D);
+    __syncthreads();
   }
 }
 
@@ -924,7 +953,7 @@ struct Layout {
   size_t part_o, part_lse, meta, bytes;
 };
 Layout stream_layout(int64_t D, int nt) {
-  const size_t blocks = static_cast<size_t>(kMaxSms) * (nt == 2 ? 3 : 2);     // Cfg::kBlocks
+  const size_t blocks = static_cast<size_t>(kMaxSms) * (nt == 1 ? 4 : nt == 2 ? 3 : 2);     // Cfg::kBlocks
   Layout l;
   l.part_o = 0;
   l.part_lse = round256(blocks * 2 * 8 * nt * D * 4);

@@ -2,7 +2,8 @@
  * fa_launch.cuh -- launch of a kernel as a programmatic dependent of the work
  * before it on the stream: its blocks may be placed while that work ends.  The
  * kernel has to call wait_for_stream() before it reads or writes memory, in
- * every thread (one that did not would let the kernel after it start early).
+ * every thread (one that did not would let the kernel after it start early),
+ * and then lets the next kernel's blocks be placed too, as its own end.
  */
 #pragma once
 #include <cuda_runtime.h>
@@ -26,5 +27,9 @@ struct Launch {
 };
 
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The next kernel on the stream may be placed once all blocks have come here (so
+// only into room that none of them still needs); it waits for this one's end.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 }  // namespace fa

@@ -4,16 +4,17 @@
  * over the data.
  *
  * Bound by HBM: 8 or so operations a value against 4 bytes moved (forward; 6
- * backward).  So one read and one write of each value, with the next rows'
- * loads always in flight:
+ * backward).  So one read and one write of each value:
+ *   - a warp takes tokens one after another (with few tokens, a part of one's
+ *     heads) and walks the query and then the key heads, 512 bytes a step; its
+ *     rows come by cp.async through a ring of steps in shared memory that runs
+ *     on over heads and tokens.  (Loads ahead in registers hid no more than one
+ *     step's time: 99 us backward at 16384 tokens of 32 + 8 heads of 128.)
  *   - a head vector lies in D / 8 lanes (16 at D = 128, 8 at 64), so sums over
  *     a head are 4 or 3 shuffles; a lane holds both values of its rotation
  *     pairs (four elements of the first half and their partners of the second,
  *     two 8-byte accesses), so the rotation needs none;
- *   - one block works out the cosines and sines of its one to four tokens, a
- *     pair a thread, in shared memory; then each warp walks heads of one token
- *     with that token's values and the weights in registers;
- *   - with few tokens more warps share one.
+ *   - a token's cosines and sines are worked out once, two pairs a lane.
  * The angle: a position times the frequency, in turns modulo 1, as a 64-bit
  * fixed-point product (wrapping is the reduction), so no position is too far
  * for 32-bit sine and cosine; in integers, as this GPU has few fp64 units.
@@ -32,10 +33,11 @@
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kFwdWarps = 8;          // warps of a block, forward
+constexpr int kBwdWarps = 4;          // and backward
 constexpr int kMaxPairs = 64;
-constexpr int kBwdResident = 2;       // blocks of the backward an SM holds
-constexpr int kBwdBlocks = 152 * kBwdResident;   // its grid: rows of the weight gradients' partial sums
+constexpr int kBwdResident = 4;       // blocks of the backward an SM holds
+constexpr int kBwdBlocks = 152 * kBwdResident;   // backward grid: rows of the weight gradients' partial sums
 
 struct RopeParams {
   const void* x[2];        // q, k: the forward's inputs
@@ -48,7 +50,7 @@ struct RopeParams {
   float* partial;          // backward: [blocks, 2, D] weight gradient partials, or null
   int64_t B, S;
   int32_t heads[2];
-  int32_t share;           // warps that share a token: 1, 2, 4 or 8
+  int32_t share;           // warps that share a token
   int32_t rot;             // rotated elements
   float eps;
   uint8_t axis[kMaxPairs]; // axis of each pair
@@ -81,12 +83,46 @@ template <> struct Pack<__nv_bfloat16> {
   }
   static __device__ __forceinline__ __nv_bfloat16 one(float x) { return __float2bfloat16_rn(x); }
 };
+// Two fp32 values in a register pair: one instruction for both (the issue slots
+// are what comes closest to HBM's time here).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float both(F2 x) {
+  const float2 v = split(x);
+  return v.x + v.y;
+}
+
+// A lane's 8 values as pairs: lo 0 1, lo 2 3, hi 0 1, hi 2 3.
 template <typename T>
-__device__ __forceinline__ void unpack(const Raw& r, float (&f)[8]) {
-  Pack<T>::load2(r.lo.x, f[0], f[1]);
-  Pack<T>::load2(r.lo.y, f[2], f[3]);
-  Pack<T>::load2(r.hi.x, f[4], f[5]);
-  Pack<T>::load2(r.hi.y, f[6], f[7]);
+__device__ __forceinline__ void unpack(const Raw& r, F2 (&f)[4]) {
+  const uint32_t w[4] = {r.lo.x, r.lo.y, r.hi.x, r.hi.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    Pack<T>::load2(w[i], a, b);
+    f[i] = f2(a, b);
+  }
 }
 
 // Which elements a lane holds: 4 from lo and 4 from hi.  Interleaved pairs are
@@ -104,9 +140,15 @@ __device__ __forceinline__ Raw load_row(const uint16_t* row, const Elements& e) 
   return Raw{*reinterpret_cast<const uint2*>(row + e.lo), *reinterpret_cast<const uint2*>(row + e.hi)};
 }
 template <typename T>
-__device__ __forceinline__ void store_row(uint16_t* row, const Elements& e, const float (&f)[8]) {
-  *reinterpret_cast<uint2*>(row + e.lo) = make_uint2(Pack<T>::store2(f[0], f[1]), Pack<T>::store2(f[2], f[3]));
-  *reinterpret_cast<uint2*>(row + e.hi) = make_uint2(Pack<T>::store2(f[4], f[5]), Pack<T>::store2(f[6], f[7]));
+__device__ __forceinline__ void store_row(uint16_t* row, const Elements& e, const F2 (&f)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = split(f[i]);
+    w[i] = Pack<T>::store2(v.x, v.y);
+  }
+  *reinterpret_cast<uint2*>(row + e.lo) = make_uint2(w[0], w[1]);
+  *reinterpret_cast<uint2*>(row + e.hi) = make_uint2(w[2], w[3]);
 }
 
 // Sum over the LANES lanes that hold one head vector.
@@ -146,48 +188,61 @@ __device__ __forceinline__ float2 angle(const RopeParams& p, int64_t token, int 
 __device__ __forceinline__ void block_angles(const RopeParams& p, int64_t token0, float2 (*table)[kMaxPairs]) {
   const int i = threadIdx.x % kMaxPairs;
   if (i >= p.rot / 2) return;
-  for (int k = threadIdx.x / kMaxPairs; k < kWarps / p.share; k += kWarps * 32 / kMaxPairs)
+  for (int k = threadIdx.x / kMaxPairs; k < kFwdWarps / p.share; k += kFwdWarps * 32 / kMaxPairs)
     if (token0 + k < p.B * p.S) table[k][i] = angle(p, token0 + k, i);
+}
+
+// The cosines and sines of a token, two pairs a lane of the warp.
+__device__ __forceinline__ void warp_angles(const RopeParams& p, int64_t token, float2* table, int lane) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (lane + 32 * j < p.rot / 2) table[lane + 32 * j] = angle(p, token, lane + 32 * j);
 }
 
 // A lane's four pairs: cosines and sines (turned back with direction -1).
 struct Turn {
-  float cs[4], sn[4];
+  F2 cs[2], sn[2], minus_sn[2];     // of pairs 0 1 and 2 3
 };
 __device__ __forceinline__ Turn load_turn(const float2* table, const Elements& e, float direction) {
   Turn t;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 v = e.pair >= 0 ? table[e.pair + j] : make_float2(1.0f, 0.0f);
-    t.cs[j] = v.x;
-    t.sn[j] = direction * v.y;
+  for (int j = 0; j < 2; ++j) {
+    const float2 a = e.pair >= 0 ? table[e.pair + 2 * j] : make_float2(1.0f, 0.0f);
+    const float2 b = e.pair >= 0 ? table[e.pair + 2 * j + 1] : make_float2(1.0f, 0.0f);
+    t.cs[j] = f2(a.x, b.x);
+    t.sn[j] = f2(direction * a.y, direction * b.y);
+    t.minus_sn[j] = f2(-direction * a.y, -direction * b.y);
   }
   return t;
 }
 template <bool INTERLEAVED>
-__device__ __forceinline__ void turn(float (&y)[8], const Turn& t) {
+__device__ __forceinline__ void turn(F2 (&y)[4], const Turn& t) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float& a = y[INTERLEAVED ? 2 * j : j];
-    float& b = y[INTERLEAVED ? 2 * j + 1 : j + 4];
-    const float x = a * t.cs[j] - b * t.sn[j];
-    b = b * t.cs[j] + a * t.sn[j];
-    a = x;
+  for (int j = 0; j < 2; ++j) {
+    if (INTERLEAVED) {                // y[2 j] and y[2 j + 1] are pairs 2 j and 2 j + 1
+      const float2 c = split(t.cs[j]), s = split(t.sn[j]), u = split(y[2 * j]), v = split(y[2 * j + 1]);
+      y[2 * j] = f2(u.x * c.x - u.y * s.x, u.y * c.x + u.x * s.x);
+      y[2 * j + 1] = f2(v.x * c.y - v.y * s.y, v.y * c.y + v.x * s.y);
+    } else {
+      const F2 a = y[j], b = y[j + 2];
+      y[j] = fma2(b, t.minus_sn[j], a * t.cs[j]);
+      y[j + 2] = fma2(a, t.sn[j], b * t.cs[j]);
+    }
   }
 }
 
 // Both weight vectors as fp32 in shared memory (ones where there is none), by the block.
-template <typename T, int D>
+template <int WARPS, typename T, int D>
 __device__ __forceinline__ void block_weights(const RopeParams& p, float (*table)[D]) {
-  for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) {
+  for (int i = threadIdx.x; i < 2 * D; i += WARPS * 32) {
     const T* src = static_cast<const T*>(p.weight[i / D]);
     table[i / D][i % D] = src ? static_cast<float>(src[i % D]) : 1.0f;
   }
 }
-__device__ __forceinline__ void load_weight(const float* table, const Elements& e, float (&w)[8]) {
+__device__ __forceinline__ void load_weight(const float* table, const Elements& e, F2 (&w)[4]) {
   const float4 a = *reinterpret_cast<const float4*>(table + e.lo), b = *reinterpret_cast<const float4*>(table + e.hi);
-  w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-  w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  w[0] = f2(a.x, a.y); w[1] = f2(a.z, a.w);
+  w[2] = f2(b.x, b.y); w[3] = f2(b.z, b.w);
 }
 
 __device__ __forceinline__ int64_t row_base(const fa_strides_t& st, int64_t b, int64_t s) {
@@ -207,14 +262,15 @@ __device__ __forceinline__ void heads_of(const RopeParams& p, int part, int whic
 constexpr int kFwdRows = 2;   // rows a lane loads ahead
 
 template <typename T, int D, bool INTERLEAVED, bool NORM>
-__global__ void __launch_bounds__(kWarps * 32, 4) fa_rope_fwd_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kFwdWarps * 32, 4) fa_rope_fwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LANES = D / 8, PER = 32 / LANES;   // lanes a head, heads a warp at once
-  __shared__ float2 table[kWarps][kMaxPairs];
+  __shared__ float2 table[kFwdWarps][kMaxPairs];
   __shared__ __align__(16) float weights[2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % LANES, slot = lane / LANES;
   fa::wait_for_stream();
-  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * (kWarps / p.share);
+  fa::let_next_start();
+  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * (kFwdWarps / p.share);
   const int mine = warp / p.share, part = warp % p.share;
   const bool real = token0 + mine < p.B * p.S;
   const uint32_t token = real ? static_cast<uint32_t>(token0 + mine) : 0u;
@@ -241,12 +297,12 @@ __global__ void __launch_bounds__(kWarps * 32, 4) fa_rope_fwd_kernel(const __gri
     };
     load(first);
     if (which == 0) {
-      if (NORM) block_weights<T, D>(p, weights);
+      if (NORM) block_weights<kFwdWarps, T, D>(p, weights);
       block_angles(p, token0, table);
       __syncthreads();
       t = load_turn(table[mine], e, 1.0f);
     }
-    float w[8];
+    F2 w[4];
     if (NORM) load_weight(weights[which], e, w);
     for (int h0 = first; h0 < last; h0 += PER * kFwdRows) {
       Raw now[kFwdRows];
@@ -256,15 +312,14 @@ __global__ void __launch_bounds__(kWarps * 32, 4) fa_rope_fwd_kernel(const __gri
 #pragma unroll
       for (int i = 0; i < kFwdRows; ++i) {
         const int h = h0 + i * PER + slot;
-        float y[8];
+        F2 y[4];
         unpack<T>(now[i], y);
         if (NORM) {
-          float ss = 0.0f;
+          const F2 ss = fma2(y[3], y[3], fma2(y[2], y[2], fma2(y[1], y[1], y[0] * y[0])));
+          const float r = rsqrtf(head_sum<LANES>(both(ss)) * (1.0f / D) + p.eps);
+          const F2 rr = f2(r, r);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss += y[j] * y[j];
-          const float r = rsqrtf(head_sum<LANES>(ss) * (1.0f / D) + p.eps);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = y[j] * r * w[j];
+          for (int j = 0; j < 4; ++j) y[j] = y[j] * rr * w[j];
         }
         turn<INTERLEAVED>(y, t);
         if (h < last) store_row<T>(dst + h * out_step, e, y);
@@ -273,115 +328,197 @@ __global__ void __launch_bounds__(kWarps * 32, 4) fa_rope_fwd_kernel(const __gri
   }
 }
 
-constexpr int kBwdRows = 2;
+// A warp's work: tasks id, id + step, ... below tasks; task = (token, part of
+// its steps).  A token's steps: PER query heads each, then PER key heads each.
+template <int PER>
+struct Walk {
+  int64_t task, step, tasks;
+  int32_t at, end, nq;          // step in the token, the task's end, steps of query heads
+  uint32_t b, s, token;
+
+  __device__ __forceinline__ Walk(const RopeParams& p) {
+    step = static_cast<int64_t>(gridDim.x) * kBwdWarps;
+    tasks = p.B * p.S * p.share;
+    nq = (p.heads[0] + PER - 1) / PER;
+    task = static_cast<int64_t>(blockIdx.x) * kBwdWarps + threadIdx.x / 32 - step;
+    at = end = 0;
+    advance_task(p);
+  }
+  __device__ __forceinline__ bool more() const { return task < tasks; }
+  // The next task that has steps (a part may have none).
+  __device__ __forceinline__ void advance_task(const RopeParams& p) {
+    const int n = nq + (p.heads[1] + PER - 1) / PER;
+    do {
+      task += step;
+      if (task >= tasks) return;
+      token = static_cast<uint32_t>(task) / static_cast<uint32_t>(p.share);
+      const int part = static_cast<int>(static_cast<uint32_t>(task) - token * p.share);
+      at = n * part / p.share;
+      end = n * (part + 1) / p.share;
+    } while (at >= end);
+    b = token / static_cast<uint32_t>(p.S);
+    s = token - b * static_cast<uint32_t>(p.S);
+  }
+  __device__ __forceinline__ int kind() const { return at >= nq; }
+  __device__ __forceinline__ int head() const { return (at >= nq ? at - nq : at) * PER; }
+};
+
+constexpr int kStepBytes = 512;         // PER heads of one tensor
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {   // zeros behind `bytes`
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// The copies' side of a walk: steps of x (forward), or of dy and, where X, x
+// into ring stages.  Addresses move on by a head stride; they are worked out
+// where a run of one kind of heads begins.
+template <int D, bool GRAD, bool X>
+struct Feed {
+  static constexpr int LANES = D / 8, PER = 32 / LANES;
+  Walk<PER> w;
+  const uint16_t *x, *dy;
+  int h, h_end, left;             // this lane's head, heads, steps left of the run (0: none)
+
+  __device__ __forceinline__ Feed(const RopeParams& p, int lane) : w(p), x(nullptr), dy(nullptr), h(0), h_end(0), left(0) {
+    begin_run(p, lane);
+  }
+  __device__ __forceinline__ void begin_run(const RopeParams& p, int lane) {
+    if (!w.more()) return;
+    const int k = w.kind();
+    h = w.head() + lane / LANES;
+    h_end = p.heads[k];
+    left = k ? w.end - w.at : min(w.end, w.nq) - w.at;
+    w.at += left;
+    const int64_t e = (lane % LANES) * 8;
+    if (X) x = static_cast<const uint16_t*>(p.x[k]) + row_base(p.st_x[k], w.b, w.s) + h * p.st_x[k].head + e;
+    if (GRAD) dy = static_cast<const uint16_t*>(p.dy[k]) + row_base(p.st_dy[k], w.b, w.s) + h * p.st_dy[k].head + e;
+  }
+  // One step (nothing once the work is all under way), as a group of its own.
+  __device__ __forceinline__ void step(const RopeParams& p, uint32_t stage, int lane) {
+    if (left > 0) {
+      const int k = w.at > w.nq;
+      const int bytes = h < h_end ? 16 : 0;
+      if (GRAD) {
+        copy16(stage + lane * 16, bytes ? dy : static_cast<const uint16_t*>(p.dy[0]), bytes);
+        dy += p.st_dy[k].head * PER;
+      }
+      if (X) {
+        copy16(stage + (GRAD ? kStepBytes : 0) + lane * 16, bytes ? x : static_cast<const uint16_t*>(p.x[0]), bytes);
+        x += p.st_x[k].head * PER;
+      }
+      h += PER;
+      if (--left == 0) {
+        if (w.at >= w.end) w.advance_task(p);
+        begin_run(p, lane);
+      }
+    }
+    copies_commit();
+  }
+};
+
+constexpr int kStages = 7;
 
 template <typename T, int D, bool INTERLEAVED, bool NORM>
-__global__ void __launch_bounds__(kWarps * 32, kBwdResident) fa_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kBwdWarps * 32, kBwdResident) fa_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LANES = D / 8, PER = 32 / LANES;
-  __shared__ float2 table[2][kWarps][kMaxPairs];
+  constexpr int kBytes = 2 * kStepBytes;
+  __shared__ __align__(128) uint8_t ring[kBwdWarps][kStages * kBytes];
+  __shared__ float2 tables[kBwdWarps][kMaxPairs];
   __shared__ __align__(16) float weights[2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % LANES, slot = lane / LANES;
   fa::wait_for_stream();
+  fa::let_next_start();
   const Elements e = elements<INTERLEAVED>(p.rot, sub);
-  const int per_block = kWarps / p.share, mine = warp / p.share, part = warp % p.share;
-  const int64_t tokens = p.B * p.S;
-  float dw[2][8];
+  const uint32_t stages = static_cast<uint32_t>(__cvta_generic_to_shared(ring[warp]));
+  Feed<D, true, NORM> ahead(p, lane);
+  Walk<PER> now(p);
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) ahead.step(p, stages + i * kBytes, lane);
+  if (NORM) {
+    block_weights<kBwdWarps, T, D>(p, weights);
+    __syncthreads();
+  }
+  F2 dw[2][4];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) dw[j / 8][j % 8] = 0.0f;
-
-  if (NORM) block_weights<T, D>(p, weights);      // (read behind the first barrier)
-  int buffer = 0;
-  for (int64_t token0 = static_cast<int64_t>(blockIdx.x) * per_block; token0 < tokens;
-       token0 += static_cast<int64_t>(gridDim.x) * per_block, buffer ^= 1) {
-    const bool real = token0 + mine < tokens;
-    const uint32_t token = real ? static_cast<uint32_t>(token0 + mine) : 0u;
-    const uint32_t b = token / static_cast<uint32_t>(p.S), s = token - b * static_cast<uint32_t>(p.S);
-    Turn t;
+  for (int j = 0; j < 8; ++j) dw[j / 4][j % 4] = f2(0.0f, 0.0f);
+  int stage = 0;
+  while (now.more()) {
+    warp_angles(p, now.token, tables[warp], lane);
+    __syncwarp();
+    const Turn t = load_turn(tables[warp], e, -1.0f);
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      int first, last;
-      heads_of<PER>(p, part, which, first, last);
-      if (!real) last = 0;
-      const int64_t x_step = p.st_x[which].head, dy_step = p.st_dy[which].head, out_step = p.st_out[which].head;
-      const uint16_t* x = static_cast<const uint16_t*>(p.x[which]) + row_base(p.st_x[which], b, s);
-      const uint16_t* dy = static_cast<const uint16_t*>(p.dy[which]) + row_base(p.st_dy[which], b, s);
-      uint16_t* dst = static_cast<uint16_t*>(p.out[which]) + row_base(p.st_out[which], b, s);
-      Raw rx[kBwdRows], rg[kBwdRows];
-      auto load = [&](int h0) {
+    for (int k = 0; k < 2; ++k) {                 // query heads, key heads
+      const int run = k ? now.end - now.at : min(now.end, now.nq) - now.at;
+      if (run <= 0) continue;
+      const int h_end = p.heads[k];
+      F2 w[4];
+      if (NORM) load_weight(weights[k], e, w);
+      const int64_t out_step = p.st_out[k].head;
+      uint16_t* const dst = static_cast<uint16_t*>(p.out[k]) + row_base(p.st_out[k], now.b, now.s);
+      int h = now.head() + slot;
+      for (int i = 0; i < run; ++i, h += PER) {
+        copies_wait<kStages - 2>();
+        __syncwarp();
+        const uint8_t* const st = ring[warp] + stage * kBytes;
+        F2 g[4], xv[4];
+        unpack<T>(load_row(reinterpret_cast<const uint16_t*>(st) + slot * D, e), g);
+        if (NORM) unpack<T>(load_row(reinterpret_cast<const uint16_t*>(st + kStepBytes) + slot * D, e), xv);
+        ahead.step(p, stages + (stage == 0 ? kStages - 1 : stage - 1) * kBytes, lane);
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+        turn<INTERLEAVED>(g, t);
+        if (NORM) {
+          F2 u[4];
 #pragma unroll
-        for (int i = 0; i < kBwdRows; ++i) {
-          const int h = h0 + i * PER + slot;
-          rx[i] = rg[i] = Raw{};
-          if (h < last) {
-            rg[i] = load_row(dy + h * dy_step, e);
-            if (NORM) rx[i] = load_row(x + h * x_step, e);
-          }
-        }
-      };
-      load(first);
-      if (which == 0) {       // (the other buffer's readers have passed this barrier since)
-        block_angles(p, token0, table[buffer]);
-        __syncthreads();
-        t = load_turn(table[buffer][mine], e, -1.0f);
-      }
-      float w[8];
-      if (NORM) load_weight(weights[which], e, w);
-      for (int h0 = first; h0 < last; h0 += PER * kBwdRows) {
-        Raw nx[kBwdRows], ng[kBwdRows];
+          for (int j = 0; j < 4; ++j) u[j] = g[j] * w[j];
+          const F2 ss = fma2(xv[3], xv[3], fma2(xv[2], xv[2], fma2(xv[1], xv[1], xv[0] * xv[0])));
+          const F2 dot = fma2(u[3], xv[3], fma2(u[2], xv[2], fma2(u[1], xv[1], u[0] * xv[0])));
+          const float r = rsqrtf(head_sum<LANES>(both(ss)) * (1.0f / D) + p.eps);
+          const float c = head_sum<LANES>(both(dot)) * (1.0f / D) * r * r;
+          // h < h_end only: a lane without a row holds zeros, which add
+          // nothing to dw unless r is infinite (0 * inf)
+          if (h < h_end) {
+            const F2 rr = f2(r, r), cc = f2(-c, -c);
 #pragma unroll
-        for (int i = 0; i < kBwdRows; ++i) { nx[i] = rx[i]; ng[i] = rg[i]; }
-        load(h0 + PER * kBwdRows);
-#pragma unroll
-        for (int i = 0; i < kBwdRows; ++i) {
-          const int h = h0 + i * PER + slot;
-          float g[8];
-          unpack<T>(ng[i], g);
-          turn<INTERLEAVED>(g, t);
-          if (NORM) {
-            float xv[8];
-            unpack<T>(nx[i], xv);
-            float ss = 0.0f, dot = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              ss += xv[j] * xv[j];
-              dot += g[j] * w[j] * xv[j];
-            }
-            const float r = rsqrtf(head_sum<LANES>(ss) * (1.0f / D) + p.eps);
-            const float c = head_sum<LANES>(dot) * (1.0f / D) * r * r;
-            // h < last only: a lane without a row holds zeros, which add
-            // nothing to dw unless r is infinite (0 * inf)
-            if (h < last) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                dw[which][j] += g[j] * xv[j] * r;
-                g[j] = r * (g[j] * w[j] - xv[j] * c);
-              }
+            for (int j = 0; j < 4; ++j) {
+              dw[k][j] = fma2(g[j] * rr, xv[j], dw[k][j]);
+              g[j] = rr * fma2(xv[j], cc, u[j]);
             }
           }
-          if (h < last) store_row<T>(dst + h * out_step, e, g);
         }
+        if (h < h_end) store_row<T>(dst + h * out_step, e, g);
       }
+      now.at += run;
     }
+    now.advance_task(p);
+    __syncwarp();                                 // the table has been read
   }
 
   if (NORM && p.partial) {
-    // The block's sums in a fixed order: lanes of the same elements, then warps.
-    __shared__ float sums[kWarps][2][D];
+    // The block's sums in a fixed order: lanes of the same elements, then warps
+    // (in the rings' place: all copies have landed).
+    copies_wait<0>();
+    __syncthreads();
+    float (*sums)[2][D] = reinterpret_cast<float (*)[2][D]>(&ring[0][0]);
+    static_assert(sizeof(ring) >= kBwdWarps * 2 * D * 4, "the sums fit in the rings");
 #pragma unroll
     for (int which = 0; which < 2; ++which)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float v = dw[which][j];
+        const float2 two = split(dw[which][j / 2]);
+        float v = j % 2 ? two.y : two.x;
 #pragma unroll
         for (int o = LANES; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (slot == 0) sums[warp][which][j < 4 ? e.lo + j : e.hi + j - 4] = v;
       }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) {
+    for (int i = threadIdx.x; i < 2 * D; i += kBwdWarps * 32) {
       float v = 0.0f;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) v += (&sums[k][0][0])[i];
+      for (int k = 0; k < kBwdWarps; ++k) v += (&sums[k][0][0])[i];
       p.partial[static_cast<int64_t>(blockIdx.x) * 2 * D + i] = v;
     }
   }
@@ -394,6 +531,7 @@ __global__ void __launch_bounds__(1024) fa_rope_dw_kernel(const float* partial, 
                                                           T* dwq, T* dwk) {
   __shared__ float sums[32][33];
   fa::wait_for_stream();
+  fa::let_next_start();
   const int e = threadIdx.x & 31, k = threadIdx.x >> 5;
   const float* src = partial + blockIdx.x * 32 + e;     // element of 2 D
   float v = 0.0f;
@@ -523,15 +661,26 @@ void fill(RopeParams& p, const int32_t* positions, const double* inv_freq, int64
 }
 
 // Warps that share a token: more while the tokens alone would not give each of
-// 152 SMs its 32 warps (backward: 16).  At 16384 tokens, 32 + 8 heads of 128:
+// 152 SMs its 32 warps.  At 16384 tokens, 32 + 8 heads of 128:
 // forward 60.0 us with one, 60.7 with two, 74.7 with four.
-int share_for(int64_t tokens) {
+int fwd_share(int64_t tokens) {
   return tokens >= 152 * 64 ? 1 : tokens >= 152 * 16 ? 2 : tokens >= 152 * 8 ? 4 : 8;
+}
+
+// Backward: parts a token's steps are cut into, so that there are tasks for all
+// warps of the grid: as few as that takes, two steps each at least.
+int bwd_share(int64_t tokens, int64_t steps) {
+  const int64_t want = (int64_t(kBwdBlocks) * kBwdWarps + tokens - 1) / tokens;
+  return static_cast<int>(std::max<int64_t>(1, std::min(want, (steps + 1) / 2)));
+}
+int64_t steps_of(int64_t H, int64_t H_kv, int64_t D) {
+  const int64_t per = 256 / D;
+  return (H + per - 1) / per + (H_kv + per - 1) / per;
 }
 
 template <typename T, int D>
 cudaError_t launch_fwd(const RopeParams& p, bool interleaved, bool norm, int64_t grid, cudaStream_t stream) {
-  const fa::Launch c(dim3(static_cast<unsigned>(grid)), kWarps * 32, 0, stream);
+  const fa::Launch c(dim3(static_cast<unsigned>(grid)), kFwdWarps * 32, 0, stream);
   if (interleaved)
     return norm ? cudaLaunchKernelEx(&c.cfg, fa_rope_fwd_kernel<T, D, true, true>, p)
                 : cudaLaunchKernelEx(&c.cfg, fa_rope_fwd_kernel<T, D, true, false>, p);
@@ -544,7 +693,7 @@ cudaError_t launch_bwd(const RopeParams& p, bool interleaved, bool norm, int64_t
                        void* dwk, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (grid > 0) {
-    const fa::Launch c(dim3(static_cast<unsigned>(grid)), kWarps * 32, 0, stream);
+    const fa::Launch c(dim3(static_cast<unsigned>(grid)), kBwdWarps * 32, 0, stream);
     if (interleaved)
       e = norm ? cudaLaunchKernelEx(&c.cfg, fa_rope_bwd_kernel<T, D, true, true>, p)
                : cudaLaunchKernelEx(&c.cfg, fa_rope_bwd_kernel<T, D, true, false>, p);
@@ -590,8 +739,8 @@ fa_status_t fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_o
   p.out[0] = q_out; p.out[1] = k_out;
   for (int i = 0; i < 2; ++i) { p.st_x[i] = strides[i]; p.st_out[i] = strides[2 + i]; }
   fill(p, positions, inv_freq, B, S, H, H_kv, rot_dim, pair_axis, eps, q_weight, k_weight);
-  p.share = share_for(B * S);
-  const int per_block = kWarps / p.share;
+  p.share = fwd_share(B * S);
+  const int per_block = kFwdWarps / p.share;
   const int64_t grid = (B * S + per_block - 1) / per_block;
   cudaError_t e;
   if (dtype == FA_DTYPE_F16)
@@ -657,9 +806,8 @@ fa_status_t fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const vo
   p.partial = want_dw ? static_cast<float*>(workspace) : nullptr;
   int64_t grid = 0;
   if (!empty) {
-    p.share = share_for(B * S);
-    const int per_block = kWarps / p.share;
-    grid = std::min<int64_t>((B * S + per_block - 1) / per_block, kBwdBlocks);
+    p.share = bwd_share(B * S, steps_of(H, H_kv, D));
+    grid = std::min<int64_t>((B * S * p.share + kBwdWarps - 1) / kBwdWarps, kBwdBlocks);
   }
   cudaError_t e;
   if (dtype == FA_DTYPE_F16)

@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(kThreads) fa_slots_kernel(const SlotParams p) 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = p.n_seqs;
   fa::wait_for_stream();
+  fa::let_next_start();
 
   // Running sums: each thread a contiguous run of requests, then the runs.
   const int per = (n + kThreads - 1) / kThreads;

@@ -211,7 +211,9 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, *, q_weight=None, k_weight
     (i, i + rot / 2), or neighbours with `interleaved`.  norm=False leaves out
     the norm, inv_freq=None the rotation.  `out`: a pair to write into, which may
     be (q, k) themselves; only where no gradient is asked for."""
-    wants = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, q_weight, k_weight))
+    wants = torch.is_grad_enabled() and (q.requires_grad or k.requires_grad
+                                         or (q_weight is not None and q_weight.requires_grad)
+                                         or (k_weight is not None and k_weight.requires_grad))
     if not wants:
         return _forward(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, pair_axis, interleaved, layout, out)
     if out is not None:
