@@ -530,8 +530,8 @@ fa_status_t fa_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales, const u
  *   Where max_seqlen_q * H / H_kv is small (decoding, a few speculative
  *   tokens) the cache is read as it is, its work split evenly over the GPU
  *   whatever the lengths; otherwise the keys and values of the sequences that
- *   bring queries are unpacked into the workspace (V with its descale, one
- *   rounding to `dtype`) and the dense tensor-core forward reads them there.
+ *   bring queries are unpacked into the workspace (exactly: code * scale fits
+ *   both types) and the packed tensor-core forward reads them there.
  *   total_k: at least the sum of seqused_k (host-known; it sizes the unpacked
  *   rows; keys past it may be left out).  At most 16384 sequences when
  *   unpacking.

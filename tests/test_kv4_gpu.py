@@ -160,14 +160,14 @@ class Step:
             k, v = (ref.gather(*a, table[s], nk, c.num_pages) for a in arrays)
             O, L, PV, A = ref.attend(q64[at:at + nq], k, v, scale, causal)
             half = ref.half_step(self.dtype)
-            p_step, v_step = (half, half) if unpacked else (ref.half_step(torch.float16), 0.0)
+            p_step, v_step = (half, 0.0) if unpacked else (ref.half_step(torch.float16), 0.0)
             bo, bl = ref.attend_bounds(O, PV, A, nk, self.D, self.dtype, p_step, v_step)
             rows = slice(at, at + nq)
             assert np.isfinite(o64[rows]).all()
             assert (np.abs(o64[rows] - O) <= bo).all(), (s, (np.abs(o64[rows] - O) / bo).max())
             assert np.array_equal(np.isneginf(L), np.isneginf(l64[:, rows]))
             fin = np.isfinite(L)
-            assert (np.abs(l64[:, rows] - L)[fin] <= bl[fin]).all()
+            assert (np.abs(l64[:, rows][fin] - L[fin]) <= bl[fin]).all()
             at += nq
         # rows of no sequence: untouched
         assert (o[at:].view(torch.int16) == CANARY16).all() and (lse[:, at:].contiguous().view(torch.int32) == CANARY32).all()

@@ -949,7 +949,7 @@ fa_status_t run_var(const void* q, const void* k, const void* v, void* o, float*
                     int64_t max_seqlen_q, int64_t H, int64_t H_kv, int64_t D, float scale,
                     int causal, fa_dtype_t dtype, const float* descale_q, const float* descale_k,
                     const float* descale_v, cudaStream_t stream, int n_splits = 1,
-                    void* workspace = nullptr, size_t workspace_bytes = 0) {
+                    void* workspace = nullptr, size_t workspace_bytes = 0, float o_scale = 1.0f) {
   const bool paged = block_table != nullptr;
   // ---- host-side checks: nothing below touches the device until they pass
   if (!q || !k || !v || !o || !lse || !cu_q) return FA_ERR_INVALID_ARG;
@@ -1058,6 +1058,7 @@ fa_status_t run_var(const void* q, const void* k, const void* v, void* o, float*
   p.n_seqs = static_cast<int32_t>(n_seqs);
   p.max_pages = static_cast<int32_t>(paged ? max_pages : 0);
   p.page_size = static_cast<int32_t>(paged ? page_size : 0);
+  p.o_scale = o_scale;
   p.seq_order = seq_order;
   if (seq_order &&
       fa::launch_seq_order(seqused_k, static_cast<int>(n_seqs), max_pages * page_size, seq_order,
@@ -1095,6 +1096,20 @@ fa_status_t run_var(const void* q, const void* k, const void* v, void* o, float*
 }
 
 }  // namespace
+
+namespace fa {
+// fa_fwd_varlen (16-bit) with O multiplied by o_scale before its rounding, for
+// values whose descale is not in v (the 4-bit cache's unpacked rows).
+fa_status_t fwd_varlen_scaled(const void* q, const void* k, const void* v, void* o, float* lse,
+                              const int32_t* cu_q, const int32_t* cu_k, int64_t n_seqs,
+                              int64_t total_q, int64_t total_k, int64_t max_seqlen_q, int64_t H,
+                              int64_t H_kv, int64_t D, float scale, int causal, fa_dtype_t dtype,
+                              float o_scale, cudaStream_t stream) {
+  return run_var(q, k, v, o, lse, cu_q, cu_k, nullptr, nullptr, n_seqs, 0, 0, 0, total_q, total_k,
+                 max_seqlen_q, H, H_kv, D, scale, causal, dtype, nullptr, nullptr, nullptr, stream,
+                 1, nullptr, 0, o_scale);
+}
+}  // namespace fa
 
 extern "C" {
 

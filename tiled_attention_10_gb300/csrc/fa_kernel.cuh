@@ -104,6 +104,7 @@ struct KernelParams {
   const int32_t* seqused_k;    // [n_seqs] keys of each sequence (paged)
   const int32_t* block_table;  // [n_seqs, max_pages] page of each key block (paged)
   int32_t n_seqs, max_pages, page_size;
+  float o_scale;               // varlen / paged, 16-bit: a factor of O (V's descale), else 1
   int32_t q_pack_log2;         // GQA packing: a query tile holds 2^q_pack_log2 heads of
                                // each of 128 >> q_pack_log2 tokens (row = token * 2^.. + head)
   int32_t causal_br;           // causal mask aligned bottom-right (key j visible to
@@ -1127,6 +1128,8 @@ __device__ void softmax_role(const KernelParams& p, const CUtensorMap* tmO, cons
     const float dv = p.descale_v ? *p.descale_v : 1.0f;
     sl2 *= dq * dk;
     o_mul = dv;  // (P's factor 256 is in l too: O / l cancels it)
+  } else if constexpr (kVar) {
+    o_mul = p.o_scale;
   }
   // A masked score is -inf and must give p = 0: keep the base-2 scale
   // strictly positive (a zero scale or descale becomes 1e-30, which changes

@@ -31,7 +31,7 @@
  *
  * Many rows (chunked prefill): bound by the matrix products.  The keys and
  * values are unpacked once into a 16-bit workspace (a few per cent of the
- * time) and the tcgen05 forward (fa_fwd_varlen) reads them there.
+ * time), exactly, and the tcgen05 forward of packed sequences reads them there.
  */
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,6 +47,15 @@
 #include "../../include/fa_api.h"
 #include "fa_kv4.cuh"
 #include "fa_launch.cuh"
+
+namespace fa {
+// The packed forward with a factor on O (fa_api.cu).
+fa_status_t fwd_varlen_scaled(const void* q, const void* k, const void* v, void* o, float* lse,
+                              const int32_t* cu_q, const int32_t* cu_k, int64_t n_seqs,
+                              int64_t total_q, int64_t total_k, int64_t max_seqlen_q, int64_t H,
+                              int64_t H_kv, int64_t D, float scale, int causal, fa_dtype_t dtype,
+                              float o_scale, cudaStream_t stream);
+}  // namespace fa
 
 namespace {
 
@@ -1083,11 +1092,9 @@ fa_status_t fa_fwd_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_
     const UnpackLayout l = unpack_layout(n_seqs, total_k, H_kv, D);
     UnpackParams u = {};
     u.cache = c;
-    // K keeps its exact values (its descale goes into the softmax scale); V
-    // takes its descale here, a second rounding to 16 bits (half a step) that
-    // O's own rounding outweighs.
-    u.cache.descale[0] = 1.0f;
-    u.cache.descale[1] = descale_v;
+    // Keys and values keep their exact values: K's descale goes into the softmax
+    // scale, V's into the factor of O before its rounding.
+    u.cache.descale[0] = u.cache.descale[1] = 1.0f;
     u.cu_q = cu_seqlens_q; u.seqused_k = seqused_k; u.block_table = block_table;
     u.cu_k = reinterpret_cast<int32_t*>(ws);
     u.out[0] = ws + l.k; u.out[1] = ws + l.v;
@@ -1101,9 +1108,8 @@ fa_status_t fa_fwd_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_
     else
       e = D == 64 ? launch_unpack<__nv_bfloat16, 64>(u, sms, stream) : launch_unpack<__nv_bfloat16, 128>(u, sms, stream);
     if (e != cudaSuccess) return FA_ERR_CUDA;
-    return fa_fwd_varlen(q, u.out[0], u.out[1], o, lse, cu_seqlens_q, u.cu_k, n_seqs, total_q, total_k,
-                         max_seqlen_q, H, H_kv, D, scale * descale_k, causal, dtype, nullptr, nullptr,
-                         nullptr, stream);
+    return fa::fwd_varlen_scaled(q, u.out[0], u.out[1], o, lse, cu_seqlens_q, u.cu_k, n_seqs, total_q, total_k,
+                                 max_seqlen_q, H, H_kv, D, scale * descale_k, causal, dtype, descale_v, stream);
   }
 
   const int nt = tiles_for(rows);
