@@ -445,7 +445,8 @@ fa_status_t fa_paged_slots(const int32_t* past_k, const int32_t* new_q, const in
  *     of 16 up to D.  norm = 0 with rot_dim = 0 is FA_ERR_INVALID_ARG.
  *   dtype: FA_DTYPE_F16 or FA_DTYPE_BF16; D 64 or 128.  fp32 arithmetic, one
  *     rounding.  B * S = 0 returns FA_OK.
- * eps finite and >= 0.  One launch.
+ * eps finite and >= 0.  One launch.  (The sum of squares is an fp32 number: a
+ * head with bf16 values beyond 1e18 or so has an infinite one, and u = 0.)
  *
  * fa_qk_norm_rope_bwd -- its gradients.  With g = dy turned back, r =
  * rsqrt(mean(x^2) + eps), h = x r:
@@ -525,7 +526,7 @@ fa_status_t fa_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales, const u
  * fa_fwd_paged_kv4 -- attention of packed queries over the 4-bit cache: q, o,
  *   lse, cu_seqlens_q, seqused_k, block_table, causal and a row without keys
  *   (O = 0, lse = -inf) as fa_fwd_paged; the cache and its descales as above.
- *   dtype: F16 or BF16 (of q and o).  Keys behind seqused_k are not looked at;
+ *   dtype: F16 or BF16 (of q and o, which must not overlap).  Keys behind seqused_k are not looked at;
  *   pages outside [0, num_pages) read as zeros.
  *   Where max_seqlen_q * H / H_kv is small (decoding, a few speculative
  *   tokens) the cache is read as it is, its work split evenly over the GPU

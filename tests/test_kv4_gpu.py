@@ -275,6 +275,35 @@ def test_a_sequences_result_does_not_depend_on_rows_behind(cuda_lib):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_two_streams_at_once(cuda_lib):
+    """Calls that overlap, each with its own workspace, give what they give alone."""
+    steps = [Step([1] * 40, list(range(900, 940)), 8, 2, 128, 16, "bf16", seed=20), Step([70, 9], [400, 800], 8, 2, 128, 32, "bf16", seed=21)]
+    alone = [st.run() for st in steps]
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, (st, stream) in enumerate(zip(steps, streams)):
+            with torch.cuda.stream(stream):
+                got[i].append(st.run())
+    torch.cuda.synchronize()
+    for a, runs in zip(alone, got):
+        for b in runs:
+            assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+
+
+def test_a_nan_query_stays_in_its_row(cuda_lib):
+    for qn in (1, 4, 80):
+        st = Step([qn, qn], [300, 200], 8, 2, 128, 16, "bf16", seed=22)
+        want = st.run()
+        st.q[qn, 3, 7] = float("nan")
+        got = st.run()
+        assert torch.isnan(got[0][qn, 3]).all()
+        keep = torch.ones(2 * qn, 8, dtype=torch.bool, device="cuda")
+        keep[qn, 3] = False
+        assert torch.equal(got[0][keep], want[0][keep]) and torch.equal(got[1].t()[keep], want[1].t()[keep])
+
+
 def test_cache_past_32_bit_offsets(cuda_lib):
     """Pages whose codes and scales start beyond 2^32 bytes."""
     pages, ps = (1 << 32) // (64 * 16) + 300, 16

@@ -140,7 +140,8 @@ def _att(**over):
     (dict(D=80), 2), (dict(dtype="e4m3"), 2), (dict(ps=48), 2), (dict(cols=1 << 28), 2), (dict(tq=1 << 31), 2),
     (dict(mq=1000, n=16385), 2),
     (dict(q=P[0] + 8), 3), (dict(ks=P[2] + 8), 3), (dict(lse=P[6] + 2), 3), (dict(ws=P[10] + 128), 3), (dict(table=P[9] + 2), 3),
-    (dict(tq=0), 0),
+    (dict(o=P[0]), 1), (dict(o=P[0] + 1024), 1),
+    (dict(tq=0), 0), (dict(tq=0, q=None, o=None, lse=None), 0),
 ])
 def test_attention_refusals(built_lib, over, code):
     assert _att(**over) == code

@@ -1066,6 +1066,10 @@ fa_status_t fa_fwd_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_
       n_seqs > INT32_MAX - 1 || max_pages_per_seq > INT32_MAX || num_pages > INT32_MAX ||
       page_size > 65536 || max_pages_per_seq * page_size > kMaxRows)
     return FA_ERR_UNSUPPORTED;
+  // Queries are read by blocks that may run after another has written its rows.
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(o);
+  const uintptr_t span = static_cast<uintptr_t>(total_q) * H * D * 2;
+  if (q0 < o0 + span && o0 < q0 + span) return FA_ERR_INVALID_ARG;
   size_t need = 0;
   const fa_status_t st = fa_fwd_paged_kv4_workspace_size(n_seqs, max_seqlen_q, total_k, H, H_kv, D, &need);
   if (st != FA_OK) return st;
