@@ -3,8 +3,10 @@
  * out of the 4-bit cache (formulas in include/fa_api.h).
  *
  * Bound by HBM (2 bytes a value one way, 9/16 the other).  Writing, a thread
- * takes one group of 16 values: two 16-byte loads, one store of 8 bytes of codes
- * and one byte of scale, so that the codes fall into whole rows.  Reading, it
+ * takes groups of 16 values: two 16-byte loads (the next group's ahead), one
+ * store of 8 bytes of codes and one byte of scale, so that the codes fall into
+ * whole rows; about 15 instructions a value are what holds it back (8192 tokens
+ * of 8 heads of 128: 12 us against 6.3 of HBM's).  Reading, it
  * takes 8 values a time, so that each store of a warp fills whole lines.
  *
  * The nearest code is decided exactly.  16-bit inputs lie on a border between
@@ -37,47 +39,71 @@ struct RowParams {
   void* out[2];            // read: K, V rows
   int64_t token_stride[2], head_stride[2];   // elements (write)
   const int64_t* slot_map;
-  int64_t n_tokens, n_groups;   // groups: n_tokens * H_kv * D / 16
-  int32_t tile;            // read: tokens of a block
+  int64_t n_tokens;
+  int32_t tile;            // tokens of a block
   int64_t n_slots;
 };
 
-// amax / (6 g) for the scale: q is that up to 2^-22; the result's place among
+// Two fp32 values in a register pair: one instruction for both.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float reciprocal(float x) {      // to 1 or 2 ulp: a guess's factor
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// amax / (6 g) for the scale: q is that up to 2^-21; the result's place among
 // numbers of at most 10 bits is that of the exact quotient.
 __device__ __forceinline__ float place_scale(float q, float g, float amax) {
   const uint32_t h = (__float_as_uint(q) + 0x1000u) & 0xffffe000u;
   const float rest = fmaf(-(__uint_as_float(h) * 6.0f), g, amax);
   return __uint_as_float(h + (rest > 0.0f ? 1u : 0u) - (rest < 0.0f ? 1u : 0u));
 }
-// a / (scale g) in [0, 8] for a code, likewise: the borders are multiples of
+// a / (scale g) in [0, 8] for two codes, likewise: the borders are multiples of
 // 1/4, so the guess is cut to multiples of 2^-6 (by adding and taking away 2^17
 // and a half) and moved off by 2^-8.
-__device__ __forceinline__ float place_code(float q, float scale, float g, float a) {
-  const float h = (q + 196608.0f) - 196608.0f;
-  const float rest = fmaf(-(h * scale), g, a);
-  float side;                                     // 0, 1/2 or 1: below, on, above
-  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(side) : "f"(rest), "f"(8.507059173023462e37f), "f"(0.5f));
-  return fmaf(side, 0.0078125f, h - 0.00390625f);
+__device__ __forceinline__ float2 place_codes(float2 q, F2 scale, F2 minus_g, F2 a) {
+  const F2 c = f2(196608.0f, 196608.0f), minus_c = f2(-196608.0f, -196608.0f);
+  const F2 h = add2(add2(f2(q.x, q.y), c), minus_c);
+  const float2 rest = split(fma2(mul2(h, scale), minus_g, a));
+  float2 side;                                    // 0, 1/2 or 1: below, on, above
+  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(side.x) : "f"(rest.x), "f"(8.507059173023462e37f), "f"(0.5f));
+  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(side.y) : "f"(rest.y), "f"(8.507059173023462e37f), "f"(0.5f));
+  return split(fma2(f2(side.x, side.y), f2(0.0078125f, 0.0078125f), add2(h, f2(-0.00390625f, -0.00390625f))));
 }
 
-// Where a group lives: its token, head and group within the row.
-template <int D>
-struct Group {
-  int64_t token;
-  int32_t head, g;
-  __device__ __forceinline__ Group(int64_t i, int H_kv) {
-    constexpr int G = D / 16;
-    g = static_cast<int>(i % G);
-    const int64_t r = i / G;
-    token = r <= 0xffffffffll ? static_cast<uint32_t>(r) / static_cast<uint32_t>(H_kv) : r / H_kv;
-    head = static_cast<int>(r - token * H_kv);
-  }
-};
-// Row index (page, head, row of the page) of a slot's head.
-__device__ __forceinline__ int64_t cache_row(const fa::kv4::Cache& c, int64_t slot, int head) {
+// Row index (page, head 0, row of the page) of a slot.
+__device__ __forceinline__ int64_t cache_row(const fa::kv4::Cache& c, int64_t slot) {
   const int64_t page = slot <= 0xffffffffll ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(c.page_size)
                                             : slot / c.page_size;
-  return (page * c.H_kv + head) * c.page_size + (slot - page * c.page_size);
+  return page * c.H_kv * c.page_size + (slot - page * c.page_size);
 }
 
 template <typename T> __device__ __forceinline__ float2 unpack(uint32_t w);
@@ -87,57 +113,101 @@ template <> __device__ __forceinline__ float2 unpack<__half>(uint32_t w) {
 template <> __device__ __forceinline__ float2 unpack<__nv_bfloat16>(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const __grid_constant__ RowParams p) {
-  fa::wait_for_stream();
-  fa::let_next_start();
-  const int which = blockIdx.y;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= p.n_groups) return;
-  const Group<D> at(i, p.cache.H_kv);
-  const int64_t slot = p.slot_map[at.token];
-  if (slot < 0 || slot >= p.n_slots) return;
-  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.in[which]) +
-                                                    at.token * p.token_stride[which] +
-                                                    at.head * p.head_stride[which] + at.g * 16);
-  const uint4 r0 = src[0], r1 = src[1];
-  const uint32_t raw[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-  float x[16], amax = 0.0f;
+// The largest magnitude of 16 values, NaN passed over.
+template <typename T> __device__ __forceinline__ float largest(const uint32_t (&w)[8]);
+template <> __device__ __forceinline__ float largest<__half>(const uint32_t (&w)[8]) {
+  __half2 m = __float2half2_rn(0.0f);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&w[j])));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+template <> __device__ __forceinline__ float largest<__nv_bfloat16>(const uint32_t (&w)[8]) {
+  __nv_bfloat162 m = __float2bfloat162_rn(0.0f);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[j])));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
+// One group of 16 values: its codes and its scale.
+template <typename T>
+__device__ __forceinline__ void encode(const uint32_t (&raw)[8], float g, uint2& codes, uint32_t& code) {
+  const float amax = largest<T>(raw);
+  const float want = place_scale(fminf(amax * reciprocal(6.0f * g), 1024.0f), g, amax);
+  uint16_t two;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(want));
+  code = two;
+  const uint32_t h2 = fa::kv4::scales_to_half(two);
+  const float scale = __low2float(*reinterpret_cast<const __half2*>(&h2));
+  codes = make_uint2(0u, 0u);
+  if (scale == 0.0f) return;
+  const float inv = reciprocal(scale * g);
+  const F2 scale2 = f2(scale, scale), minus_g = f2(-g, -g);
+  float y[16];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float2 v = unpack<T>(raw[j]);
-    x[2 * j] = v.x; x[2 * j + 1] = v.y;
-    amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));   // fmaxf passes NaN over
+    const float2 x = unpack<T>(raw[j]);
+    const float2 a = make_float2(fabsf(x.x), fabsf(x.y));
+    const float2 q = make_float2(fminf(a.x * inv, 8.0f), fminf(a.y * inv, 8.0f));   // (NaN becomes 8)
+    const float2 r = place_codes(q, scale2, minus_g, f2(a.x, a.y));
+    y[2 * j] = copysignf(r.x, x.x);
+    y[2 * j + 1] = copysignf(r.y, x.y);
   }
+  uint32_t w[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w[j])
+        : "f"(y[8 * j]), "f"(y[8 * j + 1]), "f"(y[8 * j + 2]), "f"(y[8 * j + 3]), "f"(y[8 * j + 4]),
+          "f"(y[8 * j + 5]), "f"(y[8 * j + 6]), "f"(y[8 * j + 7]));
+  codes = make_uint2(w[0], w[1]);
+}
+
+// A block writes `tile` tokens (at most 32) of K or of V; a thread walks groups.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const __grid_constant__ RowParams p) {
+  constexpr int G = D / 16, R = kThreads / G;       // groups of a head; (token, head) rows at once
+  __shared__ int64_t row[32];
+  fa::wait_for_stream();
+  fa::let_next_start();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * p.tile;
+  const int n = static_cast<int>(min(static_cast<int64_t>(p.tile), p.n_tokens - first));
+  if (threadIdx.x < n) {
+    const int64_t slot = p.slot_map[first + threadIdx.x];
+    row[threadIdx.x] = slot >= 0 && slot < p.n_slots ? cache_row(p.cache, slot) : -1;
+  }
+  const int which = blockIdx.y, group = threadIdx.x % G;
+  const int h_step = R % p.cache.H_kv, t_step = R / p.cache.H_kv;
+  int t = threadIdx.x / G / p.cache.H_kv, h = threadIdx.x / G % p.cache.H_kv;
   const float g = p.cache.descale[which];
-  const float want = place_scale(fminf(amax * __frcp_rn(6.0f * g), 1024.0f), g, amax);
-  uint16_t code;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(code) : "f"(0.0f), "f"(want));
-  const uint32_t h2 = fa::kv4::scales_to_half(code);
-  const float scale = __low2float(*reinterpret_cast<const __half2*>(&h2));
-  uint32_t lo = 0u, hi = 0u;
-  if (scale > 0.0f) {
-    const float inv = __frcp_rn(scale * g);
-    float y[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float a = fabsf(x[j]);
-      y[j] = copysignf(place_code(fminf(a * inv, 8.0f), scale, g, a), x[j]);   // fminf: NaN becomes 8
+  const uint16_t* const src = static_cast<const uint16_t*>(p.in[which]) + first * p.token_stride[which] + group * 16;
+  uint4 next[2];
+  auto load = [&]() {
+    if (t < n) {
+      const uint4* from = reinterpret_cast<const uint4*>(src + t * p.token_stride[which] + h * p.head_stride[which]);
+      next[0] = from[0];
+      next[1] = from[1];
     }
-    uint32_t w[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-          "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-          "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
-          : "=r"(w[j])
-          : "f"(y[8 * j]), "f"(y[8 * j + 1]), "f"(y[8 * j + 2]), "f"(y[8 * j + 3]), "f"(y[8 * j + 4]),
-            "f"(y[8 * j + 5]), "f"(y[8 * j + 6]), "f"(y[8 * j + 7]));
-    lo = w[0]; hi = w[1];
+  };
+  load();
+  __syncthreads();
+  while (t < n) {
+    const uint32_t raw[8] = {next[0].x, next[0].y, next[0].z, next[0].w, next[1].x, next[1].y, next[1].z, next[1].w};
+    const int64_t at = row[t];
+    const int head = h;
+    t += t_step;
+    h += h_step;
+    if (h >= p.cache.H_kv) { h -= p.cache.H_kv; ++t; }
+    load();
+    if (at < 0) continue;
+    uint2 codes;
+    uint32_t scale;
+    encode<T>(raw, g, codes, scale);
+    const uint64_t r = static_cast<uint64_t>(at) + static_cast<uint32_t>(head) * static_cast<uint32_t>(p.cache.page_size);
+    *reinterpret_cast<uint2*>(p.cache.codes[which] + r * (D / 2) + group * 8) = codes;
+    p.cache.scales[which][r * G + group] = static_cast<uint8_t>(scale);
   }
-  const int64_t row = cache_row(p.cache, slot, at.head);
-  *reinterpret_cast<uint2*>(p.cache.codes[which] + row * (D / 2) + at.g * 8) = make_uint2(lo, hi);
-  p.cache.scales[which][row * (D / 16) + at.g] = static_cast<uint8_t>(code);
 }
 
 // A block reads `tile` tokens (at most 32) of K or of V.
@@ -150,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_read_kernel(const __grid_cons
   const int n = static_cast<int>(min(static_cast<int64_t>(p.tile), p.n_tokens - first));
   if (threadIdx.x < n) {
     const int64_t slot = p.slot_map[first + threadIdx.x];
-    row[threadIdx.x] = slot >= 0 && slot < p.n_slots ? cache_row(p.cache, slot, 0) : -1;
+    row[threadIdx.x] = slot >= 0 && slot < p.n_slots ? cache_row(p.cache, slot) : -1;
   }
   __syncthreads();
   const int which = blockIdx.y;
@@ -175,8 +245,7 @@ fa_status_t check_rows(const void* k, const void* v, const int64_t* slot_map, co
   if (dtype == FA_DTYPE_FP8E4M3 || !fa::kv4::page_size_ok(page_size)) return FA_ERR_UNSUPPORTED;
   if (off(k, 16) || off(v, 16) || off(slot_map, 8) || off(kc, 16) || off(vc, 16) || off(ks, 16) || off(vs, 16))
     return FA_ERR_MISALIGNED;
-  if (page_size > 65536 || num_pages > INT32_MAX || H_kv > 65536 || n_tokens > INT32_MAX ||
-      n_tokens * H_kv * (D / 16) > static_cast<int64_t>(INT32_MAX) * kThreads)
+  if (page_size > 65536 || num_pages > INT32_MAX || H_kv > 65536 || n_tokens > INT32_MAX)
     return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
@@ -193,7 +262,9 @@ RowParams params(const uint8_t* kc, const uint8_t* ks, const uint8_t* vc, const 
   p.cache.H_kv = static_cast<int32_t>(H_kv);
   p.slot_map = slot_map;
   p.n_tokens = n_tokens;
-  p.n_groups = n_tokens * H_kv * (D / 16);
+  // 32 tokens a block, or fewer while that leaves SMs idle
+  p.tile = 32;
+  while (p.tile > 1 && n_tokens < int64_t(p.tile) * 152 * 4) p.tile /= 2;
   p.n_slots = num_pages * page_size;
   return p;
 }
@@ -228,7 +299,7 @@ fa_status_t fa_kv4_write(const void* k, const void* v, const int64_t* slot_map, 
                        n_tokens, H_kv, D, page_size, num_pages);
   p.in[0] = k; p.in[1] = v;
   for (int i = 0; i < 2; ++i) { p.token_stride[i] = strides[i].seq; p.head_stride[i] = strides[i].head; }
-  const int64_t blocks = (p.n_groups + kThreads - 1) / kThreads;
+  const int64_t blocks = (n_tokens + p.tile - 1) / p.tile;
   if (dtype == FA_DTYPE_F16)
     return D == 64 ? launch(fa_kv4_write_kernel<__half, 64>, p, blocks, stream)
                    : launch(fa_kv4_write_kernel<__half, 128>, p, blocks, stream);
@@ -248,9 +319,6 @@ fa_status_t fa_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales, const u
   RowParams p = params(k_codes, k_scales, v_codes, v_scales, descale_k, descale_v, slot_map,
                        n_tokens, H_kv, D, page_size, num_pages);
   p.out[0] = k_out; p.out[1] = v_out;
-  // 32 tokens a block, or fewer while that leaves SMs idle
-  p.tile = 32;
-  while (p.tile > 1 && n_tokens < int64_t(p.tile) * 152 * 2) p.tile /= 2;
   const int64_t blocks = (n_tokens + p.tile - 1) / p.tile;
   if (dtype == FA_DTYPE_F16)
     return D == 64 ? launch(fa_kv4_read_kernel<__half, 64>, p, blocks, stream)
