@@ -1098,6 +1098,17 @@ fa_status_t run_var(const void* q, const void* k, const void* v, void* o, float*
 }  // namespace
 
 namespace fa {
+// The current device's error word for bounded waits, and their limit.
+fa_status_t wait_control(uint32_t** err, uint64_t* limit_ns) {
+  DeviceInfo dev;
+  if (device_info(&dev) != FA_OK) return FA_ERR_CUDA;
+  *err = dev.err_word;
+  *limit_ns = g_wait_limit_ns.load();
+  return FA_OK;
+}
+}  // namespace fa
+
+namespace fa {
 // fa_fwd_varlen (16-bit) with O multiplied by o_scale before its rounding, for
 // values whose descale is not in v (the 4-bit cache's unpacked rows).
 fa_status_t fwd_varlen_scaled(const void* q, const void* k, const void* v, void* o, float* lse,

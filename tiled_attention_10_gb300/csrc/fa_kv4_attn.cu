@@ -45,8 +45,8 @@
 #include <type_traits>
 
 #include "../../include/fa_api.h"
-#include "fa_kv4.cuh"
-#include "fa_launch.cuh"
+#include "fa_kv4_units.cuh"
+#include "fa_kv4_wide.cuh"
 
 namespace fa {
 // The packed forward with a factor on O (fa_api.cu).
@@ -55,79 +55,15 @@ fa_status_t fwd_varlen_scaled(const void* q, const void* k, const void* v, void*
                               int64_t total_q, int64_t total_k, int64_t max_seqlen_q, int64_t H,
                               int64_t H_kv, int64_t D, float scale, int causal, fa_dtype_t dtype,
                               float o_scale, cudaStream_t stream);
+// The current device's error word for bounded waits, and their limit (fa_api.cu).
+fa_status_t wait_control(uint32_t** err, uint64_t* limit_ns);
 }  // namespace fa
 
 namespace {
 
-using fa::kv4::Cache;
-using fa::kv4::codes_to_half;
-using fa::kv4::mul_half;
-using fa::kv4::scales_to_half;
+using namespace fa::kv4;
 
 constexpr int kStep = 32;           // keys of a warp's step
-constexpr int kChunk = 64;          // keys of a unit of work
-constexpr int kUnitCost = 6;        // chunks that a unit costs beside its own, for an even split
-constexpr int kMinShare = kUnitCost + 1;   // least work of a block, in chunks: any run longer than
-                                    // kUnitCost holds keys
-constexpr int kMaxSms = 160;
-constexpr float kBias = 8.0f;       // P is held as 2^(score - max + kBias): small
-                                    // probabilities stay normal numbers of f16
-constexpr float kLag = 6.0f;        // the maximum follows once a score passes it by
-                                    // this much (log2): P <= 2^14 < 65504
-
-struct AttnParams {
-  Cache cache;
-  const void* q;
-  void* o;
-  float* lse;
-  const int32_t* cu_q;
-  const int32_t* seqused_k;
-  const int32_t* block_table;
-  float* part_o;          // [blocks, 2, rows, D]
-  float* part_lse;        // [blocks, 2, rows]
-  struct Meta* meta;      // [blocks]
-  int64_t total_q, max_keys;
-  float sl2;              // |scale| * descale_k * log2(e)
-  int32_t n_seqs, max_pages, page_shift;   // page_shift: log2(page_size), or -1
-  int32_t H, G, causal, negate;            // G = H / H_kv
-};
-
-// A unit that starts in this block's run and ends in a later block's.
-struct Meta {
-  int64_t q_row0;    // the sequence's first row of q
-  int32_t pieces;    // 0: none
-  int32_t head0;     // first query head of the group
-  int32_t row0;      // first row (token * G + head) of the tile
-  int32_t rows;      // rows of the tile that exist
-};
-
-struct Seq {
-  int64_t q_row0;
-  int32_t q_len, k_len;    // k_len: keys some row sees
-  int32_t keys;            // keys held (the causal offset counts from here)
-  int32_t tiles, chunks;   // row tiles; 64-key chunks (at least 1 where there are rows)
-};
-
-template <int ROWS>
-__device__ __forceinline__ Seq sequence(const AttnParams& p, int s) {
-  Seq q;
-  const int64_t a = min(max(static_cast<int64_t>(p.cu_q[s]), int64_t(0)), p.total_q);
-  const int64_t b = min(max(static_cast<int64_t>(p.cu_q[s + 1]), a), p.total_q);
-  q.q_row0 = a;
-  q.q_len = static_cast<int32_t>(b - a);
-  q.keys = static_cast<int32_t>(min(max(static_cast<int64_t>(p.seqused_k[s]), int64_t(0)), p.max_keys));
-  q.k_len = q.keys;
-  if (p.causal == FA_CAUSAL_TOP_LEFT) q.k_len = min(q.k_len, q.q_len);
-  q.tiles = static_cast<int32_t>((static_cast<int64_t>(q.q_len) * p.G + ROWS - 1) / ROWS);
-  q.chunks = q.q_len > 0 ? max(1, (q.k_len + kChunk - 1) / kChunk) : 0;
-  return q;
-}
-
-// A sequence's work, in chunks: its units' keys and their fixed costs.
-__device__ __forceinline__ int64_t work_of(const AttnParams& p, const Seq& q) {
-  return q.chunks > 0 ? static_cast<int64_t>(p.cache.H_kv) * q.tiles * (q.chunks + kUnitCost) : 0;
-}
-
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -155,11 +91,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t pack_half(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 template <int D>
 struct Stage {
   static constexpr int kCodes = kStep * D / 2;       // bytes of K (or V) codes
@@ -262,7 +193,7 @@ struct Cfg {
   // (128 registers) 214, 6 x 2 211, 2 x 4 224; 4000 of 256 keys, where units
   // end often: 383, 557, 354, 525; one of 65536: 28, 26, 32, 27.
   static constexpr int kWarps = NT == 1 ? 3 : 4;
-  static constexpr int kBlocks = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+  static constexpr int kBlocks = NT == 1 ? 4 : 3;
   // A warp's ring: three stages; at the end of a unit its O lies in the third
   // one's place (and behind it), while the next unit's first two steps are
   // already on their way to the other two.
@@ -272,77 +203,6 @@ struct Cfg {
   static constexpr int kQ = kWarps * kWarpBytes;                  // the unit's Q, f16, in operand order
   static constexpr int kSmem = kQ + kRows * D * 2;
 };
-
-// One unit of work: a run of chunks of one (sequence, head, row tile).
-struct Unit {
-  int64_t q_row0;                   // the sequence's first row of q
-  int32_t s, head, row0, rows;      // row0: first row (token * G + head) of the tile
-  int32_t key_begin, key_end;
-  int32_t keys, q_len, k_len;       // of the sequence, see Seq
-  int32_t piece;                    // -1: the whole (sequence, head, tile); else the partial's slot
-  int32_t pieces;                   // of a divided one that starts here, else 0
-  int32_t more;                     // another unit of this block follows
-};
-
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {   // both >= 0
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
-// An even split of the work: the first `extra` blocks have share + 1 places.
-struct Split {
-  int64_t share, extra;
-  __device__ __forceinline__ int64_t start(int64_t block) const { return share * block + min(block, extra); }
-  __device__ __forceinline__ int64_t block_of(int64_t place) const {
-    const int64_t edge = extra * (share + 1);
-    return place < edge ? divide(place, share + 1) : extra + divide(place - edge, share);
-  }
-};
-
-// Where a block is in its run of chunks.
-struct Cursor {
-  int64_t w, w1, off;       // next place, end; offset in the sequence
-  Split split;
-  int32_t s;
-  Seq sq;
-};
-
-// The cursor's next unit (moving on to the sequence that has it).
-template <int ROWS>
-__device__ __noinline__ void next_unit(const AttnParams& p, Cursor& c, Unit& u) {
-  int64_t all = work_of(p, c.sq);
-  while (c.off >= all) {
-    c.off -= all;
-    c.sq = sequence<ROWS>(p, ++c.s);
-    all = work_of(p, c.sq);
-  }
-  const Seq& sq = c.sq;
-  // A unit is kUnitCost places without keys and then its chunks; this block's
-  // run covers its places [pos, end).
-  const int size = sq.chunks + kUnitCost;
-  const int64_t unit = divide(c.off, size);
-  const int pos = static_cast<int>(c.off - unit * size);
-  const int end = static_cast<int>(min(static_cast<int64_t>(size), pos + (c.w1 - c.w)));
-  const int c0 = max(pos - kUnitCost, 0), c1 = end - kUnitCost;
-  u.q_row0 = sq.q_row0;
-  u.s = c.s;
-  u.head = static_cast<int>(divide(unit, sq.tiles));
-  u.row0 = static_cast<int>(unit - static_cast<int64_t>(u.head) * sq.tiles) * ROWS;
-  u.rows = static_cast<int>(min(static_cast<int64_t>(ROWS), static_cast<int64_t>(sq.q_len) * p.G - u.row0));
-  u.key_begin = c0 * kChunk;
-  u.key_end = min(c1 * kChunk, sq.k_len);
-  u.keys = sq.keys;
-  u.q_len = sq.q_len;
-  u.k_len = sq.k_len;
-  // a block's first unit may continue one, its last may be continued
-  u.piece = c0 > 0 ? 0 : c1 < sq.chunks ? 1 : -1;
-  u.pieces = 0;
-  if (u.piece == 1)   // up to the block that holds the unit's last chunk
-    u.pieces = static_cast<int32_t>(c.split.block_of(c.w - pos + size - 1) - blockIdx.x + 1);
-  c.w += end - pos;
-  c.off += end - pos;
-  u.more = c.w1 - c.w > kUnitCost;    // (what is left begins with a unit: has it keys?)
-}
 
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, Cfg<D, NT>::kBlocks)
@@ -363,54 +223,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, Cfg<D, NT>::kBlocks)
   fa::wait_for_stream();
   fa::let_next_start();
 
-  // ---- this block's run of the work and the sequence it starts in
-  {
-    const int per = (p.n_seqs + kWarps * 32 - 1) / (kWarps * 32);
-    const int s0 = min(p.n_seqs, tid * per), s1 = min(p.n_seqs, s0 + per);
-    int64_t mine = 0;
-    Seq sq = {};
-    for (int s = s0; s < s1; ++s) {
-      sq = sequence<kRows>(p, s);
-      mine += work_of(p, sq);
-    }
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t a = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += a;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    int64_t before = incl - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += scan[w];
-      total += scan[w];
-    }
-    const int64_t blocks = total == 0 ? 0 : min(static_cast<int64_t>(gridDim.x), max(divide(total, kMinShare), int64_t(1)));
-    const int64_t bid = blockIdx.x;
-    if (tid == 0) p.meta[bid].pieces = 0;
-    if (bid >= blocks) return;
-    const int64_t share = divide(total, blocks);
-    const Split split{share, total - share * blocks};
-    const int64_t w = split.start(bid);
-    if (w >= before && w < before + mine) {   // one thread has the sequence
-      int64_t off = w - before;
-      int s = s0;
-      if (per > 1) {                          // (else sq is the one sequence already)
-        for (;; ++s) {
-          sq = sequence<kRows>(p, s);
-          const int64_t c = work_of(p, sq);
-          if (off < c) break;
-          off -= c;
-        }
-      }
-      cursor = Cursor{w, split.start(bid + 1), off, split, s, sq};
-      next_unit<kRows>(p, cursor, units[0]);
-      if (units[0].more) next_unit<kRows>(p, cursor, units[1]);
-    }
-    __syncthreads();
-  }
+  if (!begin_units<kRows, kWarps * 32>(p, scan, cursor, units)) return;
 
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kWarpBytes;
   uint8_t* const ring_p = smem + warp * C::kWarpBytes;
@@ -773,82 +586,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, Cfg<D, NT>::kBlocks)
   }
 }
 
-// Merge of a divided unit's pieces:
-//   lse = log sum exp(lse_i),  O = sum exp(lse_i - lse) O_i.
-// The first piece is the starting block's second slot, the others the
-// following blocks' first slots.  One block a unit; its warps share the rows,
-// several on one row where there are few, each over every n-th piece.
-constexpr int kMergeWarps = 16;
-
-template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(kMergeWarps * 32) fa_kv4_merge_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int E = D / 32;              // elements a lane
-  __shared__ float sum_o[kMergeWarps][D], sum_w[kMergeWarps];
-  fa::wait_for_stream();
-  fa::let_next_start();
-  const Meta mt = p.meta[blockIdx.x];
-  if (mt.pieces == 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int share = 1;                         // warps a row
-  while (2 * share * mt.rows <= kMergeWarps && share < 8) share *= 2;
-  const int64_t first = blockIdx.x;
-  for (int base = 0; base < mt.rows; base += kMergeWarps / share) {
-    const int r = base + warp / share, part = warp % share;
-    const bool in = r < mt.rows;
-    auto at = [&](int i) { return ((first + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + r; };
-    float top = -CUDART_INF_F, sum = 0.0f, acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    if (in) {
-      for (int i = lane; i < mt.pieces; i += 32) top = fmaxf(top, p.part_lse[at(i)]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-#pragma unroll 8
-      for (int i = part; i < mt.pieces; i += share) {
-        const int64_t a = at(i);
-        const float lse = p.part_lse[a];
-        const float wgt = lse == -CUDART_INF_F ? 0.0f : expf(lse - top);
-        const float* src = p.part_o + a * D + lane * E;
-        sum += wgt;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += wgt * src[e];
-      }
-    }
-    if (share > 1) {                     // the row's warps, in order
-#pragma unroll
-      for (int e = 0; e < E; ++e) sum_o[warp][lane * E + e] = acc[e];
-      if (lane == 0) sum_w[warp] = sum;
-      __syncthreads();
-      if (part == 0 && in) {
-        for (int k = 1; k < share; ++k) {
-          sum += sum_w[warp + k];
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += sum_o[warp + k][lane * E + e];
-        }
-      }
-    }
-    if (in && part == 0) {
-      const int row = mt.row0 + r, tok = row / p.G, h = mt.head0 + (row - tok * p.G);
-      const float mul = sum == 0.0f ? 0.0f : p.cache.descale[1] / sum;
-      uint16_t* dst = static_cast<uint16_t*>(p.o) + ((mt.q_row0 + tok) * p.H + h) * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        uint32_t w;
-        if (std::is_same<T, __half>::value) {
-          w = pack_half(acc[e] * mul, acc[e + 1] * mul);
-        } else {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(acc[e] * mul, acc[e + 1] * mul);
-          w = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        *reinterpret_cast<uint32_t*>(dst + e) = w;
-      }
-      if (lane == 0)
-        p.lse[static_cast<int64_t>(h) * p.total_q + mt.q_row0 + tok] = sum == 0.0f ? -CUDART_INF_F : top + logf(sum);
-    }
-    // (share > 1 only where one pass takes all rows: the buffers are not reused)
-  }
-}
-
 // ---------------------------------------------------------------- unpacking
 constexpr int kUnpackThreads = 256;
 constexpr int kUnpackRows = 32;           // packed rows of a block
@@ -935,9 +672,9 @@ __global__ void __launch_bounds__(kUnpackThreads) fa_kv4_unpack_kernel(const __g
 }
 
 // ---------------------------------------------------------------- host
-// Rows of a sequence (queries x G) up to which the cache is read as it is:
-// measured below.
-constexpr int64_t kStreamRows = 64;
+// Rows of a sequence (queries x G) up to which the cache is read straight into
+// mma.sync operands, and up to which it is unpacked on the way to tcgen05.
+constexpr int64_t kNarrowRows = 16, kStreamRows = 128;
 constexpr int64_t kMaxUnpackSeqs = 16384;
 
 bool off(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
@@ -956,17 +693,19 @@ int sm_count() {
   return std::min(n, kMaxSms);
 }
 
-int tiles_for(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+// 8-row tiles of a unit; 0: the many-rows kernel.
+int tiles_for(int64_t rows) { return rows <= 8 ? 1 : rows <= kNarrowRows ? 2 : 0; }
 
 struct Layout {
   size_t part_o, part_lse, meta, bytes;
 };
 Layout stream_layout(int64_t D, int nt) {
-  const size_t blocks = static_cast<size_t>(kMaxSms) * (nt == 1 ? 4 : nt == 2 ? 3 : 2);     // Cfg::kBlocks
+  const size_t blocks = static_cast<size_t>(kMaxSms) * (nt == 1 ? 4 : nt == 2 ? 3 : 1);     // Cfg::kBlocks
+  const size_t rows = blocks * 2 * (nt ? 8 * nt : kWideRows);
   Layout l;
   l.part_o = 0;
-  l.part_lse = round256(blocks * 2 * 8 * nt * D * 4);
-  l.meta = l.part_lse + round256(blocks * 2 * 8 * nt * 4);
+  l.part_lse = round256(rows * D * 4);
+  l.meta = l.part_lse + round256(rows * 4);
   l.bytes = l.meta + round256(blocks * sizeof(Meta));
   return l;
 }
@@ -997,9 +736,7 @@ cudaError_t launch_stream(const AttnParams& p, int sms, cudaStream_t stream) {
 
 template <typename T, int D>
 cudaError_t launch_stream_rows(const AttnParams& p, int nt, int sms, cudaStream_t stream) {
-  return nt == 1   ? launch_stream<T, D, 1>(p, sms, stream)
-         : nt == 2 ? launch_stream<T, D, 2>(p, sms, stream)
-                   : launch_stream<T, D, 4>(p, sms, stream);
+  return nt == 1 ? launch_stream<T, D, 1>(p, sms, stream) : launch_stream<T, D, 2>(p, sms, stream);
 }
 
 template <typename T, int D>
@@ -1140,7 +877,12 @@ fa_status_t fa_fwd_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_
   p.G = static_cast<int32_t>(G);
   p.causal = causal;
   cudaError_t e;
-  if (dtype == FA_DTYPE_F16)
+  if (nt == 0) {
+    uint32_t* err = nullptr;
+    uint64_t limit_ns = 0;
+    if (fa::wait_control(&err, &limit_ns) != FA_OK) return FA_ERR_CUDA;
+    e = launch_wide(p, static_cast<int>(D), dtype == FA_DTYPE_F16, sms, err, limit_ns, stream);
+  } else if (dtype == FA_DTYPE_F16)
     e = D == 64 ? launch_stream_rows<__half, 64>(p, nt, sms, stream) : launch_stream_rows<__half, 128>(p, nt, sms, stream);
   else
     e = D == 64 ? launch_stream_rows<__nv_bfloat16, 64>(p, nt, sms, stream)
