@@ -528,11 +528,12 @@ fa_status_t fa_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales, const u
  *   (O = 0, lse = -inf) as fa_fwd_paged; the cache and its descales as above.
  *   dtype: F16 or BF16 (of q and o, which must not overlap).  Keys behind seqused_k are not looked at;
  *   pages outside [0, num_pages) read as zeros.
- *   Where max_seqlen_q * H / H_kv is small (decoding, a few speculative
- *   tokens) the cache is read as it is, its work split evenly over the GPU
- *   whatever the lengths; otherwise the keys and values of the sequences that
- *   bring queries are unpacked into the workspace (exactly: code * scale fits
- *   both types) and the packed tensor-core forward reads them there.
+ *   Where max_seqlen_q * H / H_kv is small (at most 128: decoding, speculative
+ *   tokens; at most 512 where total_k >= 2048 n_seqs) the cache is read as it
+ *   is, its work split evenly over the GPU whatever the lengths; otherwise the
+ *   keys and values of the sequences that bring queries are unpacked into the
+ *   workspace (exactly: code * scale fits both types) and the packed
+ *   tensor-core forward reads them there.
  *   total_k: at least the sum of seqused_k (host-known; it sizes the unpacked
  *   rows; keys past it may be left out).  At most 16384 sequences when
  *   unpacking.

@@ -211,6 +211,43 @@ def test_long_queries_are_unpacked(cuda_lib, dtype, D, causal):
     st.check(*st.run(causal), causal)
 
 
+@pytest.mark.parametrize("causal", [0, 1, 2])
+@pytest.mark.parametrize("heads,qmax,dtype,D,ps", [((8, 1), 3, "bf16", 128, 16), ((4, 2), 9, "f16", 64, 32), ((28, 4), 18, "bf16", 64, 64),
+                                                   ((5, 1), 25, "f16", 128, 384), ((2, 2), 128, "bf16", 128, 64)], ids=str)
+def test_17_to_128_rows(cuda_lib, heads, qmax, dtype, D, ps, causal):
+    st = Step([qmax, 1, 0, qmax - 1, qmax, 2], [700, 129, 40, qmax - 2, 128, 0], *heads, D, ps, dtype, seed=qmax, extra_rows=3)
+    st.check(*st.run(causal), causal, unpacked=False)
+
+
+@pytest.mark.parametrize("n", [1, 63, 64, 127, 128, 129, 255, 256, 257, 4097, 20000])
+def test_40_rows_over_any_length(cuda_lib, n):
+    st = Step([10], [n], 8, 2, 128, 64, "bf16", seed=n)
+    st.check(*st.run(), unpacked=False)
+
+
+def test_more_rows_over_long_sequences(cuda_lib):
+    """Several tiles of rows over sequences long enough to stay in the cache's format."""
+    st = Step([128, 31, 0], [7000, 900, 5], 8, 2, 128, 64, "bf16", seed=30)
+    st.check(*st.run(), unpacked=False)
+
+
+@pytest.mark.parametrize("std,mul", [(30.0, 1.0), (1.0, 1e-30), (1.0, 1e30)])
+def test_magnitudes_of_many_rows(cuda_lib, std, mul):
+    st = Step([9, 12, 2], [700, 64, 90], 4, 1, 128, 32, "bf16", seed=5, std=std, kd=0.003 * std)
+    st.q.mul_(mul)
+    scale = 128 ** -0.5 / mul
+    st.check(*st.run(scale=scale), scale=scale, unpacked=False)
+
+
+@pytest.mark.parametrize("lens", [[30000], [513] * 40, list(range(1, 200, 3)), [128] * 300])
+def test_any_split_of_many_rows(cuda_lib, lens):
+    st = Step([5] * len(lens), lens, 8, 2, 64, 16, "f16", seed=8)
+    o, lse = st.run()
+    st.check(o, lse)
+    again = st.run()
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])       # deterministic
+
+
 def test_both_ways_agree_at_the_border(cuda_lib):
     """The same queries through the cache as it is and, with a larger max_seqlen_q, unpacked."""
     st = Step([8, 3], [700, 90], 8, 2, 128, 64, "bf16", seed=3)
@@ -277,11 +314,12 @@ def test_a_sequences_result_does_not_depend_on_rows_behind(cuda_lib):
 
 def test_two_streams_at_once(cuda_lib):
     """Calls that overlap, each with its own workspace, give what they give alone."""
-    steps = [Step([1] * 40, list(range(900, 940)), 8, 2, 128, 16, "bf16", seed=20), Step([70, 9], [400, 800], 8, 2, 128, 32, "bf16", seed=21)]
+    steps = [Step([1] * 40, list(range(900, 940)), 8, 2, 128, 16, "bf16", seed=20), Step([70, 9], [400, 800], 8, 2, 128, 32, "bf16", seed=21),
+             Step([9] * 20, list(range(900, 920)), 8, 2, 64, 16, "bf16", seed=23)]
     alone = [st.run() for st in steps]
     streams = [torch.cuda.Stream() for _ in steps]
     torch.cuda.synchronize()
-    got = [[], []]
+    got = [[] for _ in steps]
     for _ in range(10):
         for i, (st, stream) in enumerate(zip(steps, streams)):
             with torch.cuda.stream(stream):
@@ -293,7 +331,7 @@ def test_two_streams_at_once(cuda_lib):
 
 
 def test_a_nan_query_stays_in_its_row(cuda_lib):
-    for qn in (1, 4, 80):
+    for qn in (1, 4, 20, 80):
         st = Step([qn, qn], [300, 200], 8, 2, 128, 16, "bf16", seed=22)
         want = st.run()
         st.q[qn, 3, 7] = float("nan")

@@ -1,6 +1,6 @@
 /*
  * fa_kv4_attn.cu -- fa_fwd_paged_kv4: attention of packed queries over the
- * 4-bit paged cache (include/fa_api.h).  Two ways, by the rows (queries x
+ * 4-bit paged cache (include/fa_api.h).  Three ways, by the rows (queries x
  * heads that share a key/value head) a sequence brings to each key:
  *
  * Few rows (decoding, speculative tokens): bound by HBM, 9/16 byte a cached
@@ -28,6 +28,8 @@
  * (sequence, head) that a cut divides leaves fp32 partials that a second
  * kernel merges.  A block's warps take 32-key steps in turn, each with its own
  * cp.async ring and its own running maximum, and join at the run's end.
+ *
+ * More rows (17 to 128, to 512 over long sequences): fa_kv4_wide.cu.
  *
  * Many rows (chunked prefill): bound by the matrix products.  The keys and
  * values are unpacked once into a 16-bit workspace (a few per cent of the
@@ -187,9 +189,8 @@ __device__ __forceinline__ void load_step(const AttnParams& p, const Lane& me, u
 template <int D, int NT>
 struct Cfg {
   static constexpr int kRows = 8 * NT;
-  // Warps of a block and resident blocks an SM: 12 warps of 168 registers with 8
-  // or 16 rows, 8 of 255 with 32 (O and the ring grow).  With 8 rows, 128
-  // sequences of 8192 keys (floor 178 us): 4 blocks of 3 warps 210 us, 2 x 8
+  // Warps of a block and resident blocks an SM: 12 warps of 168 registers (O and
+  // the ring grow with the rows).  With 8 rows, 128 sequences of 8192 keys (floor 178 us): 4 blocks of 3 warps 210 us, 2 x 8
   // (128 registers) 214, 6 x 2 211, 2 x 4 224; 4000 of 256 keys, where units
   // end often: 383, 557, 354, 525; one of 65536: 28, 26, 32, 27.
   static constexpr int kWarps = NT == 1 ? 3 : 4;
@@ -673,8 +674,18 @@ __global__ void __launch_bounds__(kUnpackThreads) fa_kv4_unpack_kernel(const __g
 
 // ---------------------------------------------------------------- host
 // Rows of a sequence (queries x G) up to which the cache is read straight into
-// mma.sync operands, and up to which it is unpacked on the way to tcgen05.
-constexpr int64_t kNarrowRows = 16, kStreamRows = 128;
+// mma.sync operands, up to which it is unpacked on the way to tcgen05, and up to
+// which it is so where the sequences are long (total_k a sequence): a workspace
+// of 16-bit rows costs what it writes and reads, a 128-row tile its unpacking.
+// us, tiles / workspace, D 128, H 32 / 8: 128 sequences of 8192 keys 32 rows 512
+// (508 in mma.sync operands), 64 rows 513, 128 rows 536 / 1450, 256 rows
+// 1040 / 1600, 512 rows 2050 / 2300; 32 of 2048 256 rows 110 / 132, 512 rows
+// 187 / 195; 8 of 2048 256 rows 49 / 47, 512 rows 68 / 52; one of 65536 256
+// rows 107 / 690; 256 of 256 256 rows 248 / 165.
+constexpr int64_t kNarrowRows = 16, kStreamRows = 128, kLongStreamRows = 512, kLongKeys = 2048;
+bool streams(int64_t rows, int64_t n_seqs, int64_t total_k) {
+  return rows <= (total_k / kLongKeys >= n_seqs ? kLongStreamRows : kStreamRows);
+}
 constexpr int64_t kMaxUnpackSeqs = 16384;
 
 bool off(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
@@ -767,8 +778,8 @@ fa_status_t fa_fwd_paged_kv4_workspace_size(int64_t n_seqs, int64_t max_seqlen_q
   if (max_seqlen_q > kMaxRows || total_k > kMaxRows || H > 65536 || n_seqs > INT32_MAX - 1)
     return FA_ERR_UNSUPPORTED;
   const int64_t rows = max_seqlen_q * (H / H_kv);
-  *workspace_bytes = rows <= kStreamRows ? stream_layout(D, tiles_for(rows)).bytes
-                                         : unpack_layout(n_seqs, total_k, H_kv, D).bytes;
+  *workspace_bytes = streams(rows, n_seqs, total_k) ? stream_layout(D, tiles_for(rows)).bytes
+                                                    : unpack_layout(n_seqs, total_k, H_kv, D).bytes;
   return FA_OK;
 }
 
@@ -813,7 +824,7 @@ fa_status_t fa_fwd_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_
   if (workspace_bytes < need) return FA_ERR_INVALID_ARG;
   if (off(workspace, 256)) return FA_ERR_MISALIGNED;
   const int64_t G = H / H_kv, rows = max_seqlen_q * G;
-  if (rows > kStreamRows && n_seqs > kMaxUnpackSeqs) return FA_ERR_UNSUPPORTED;
+  if (!streams(rows, n_seqs, total_k) && n_seqs > kMaxUnpackSeqs) return FA_ERR_UNSUPPORTED;
   // a row's index in the cache is a 32-bit number (2^32 rows of D = 64, K and V, take 309 GB)
   if (num_pages > static_cast<int64_t>(0xffffffffu) / (page_size * H_kv)) return FA_ERR_UNSUPPORTED;
   if (n_seqs > static_cast<int64_t>(0xffffffffu) / max_pages_per_seq) return FA_ERR_UNSUPPORTED;
@@ -829,7 +840,7 @@ fa_status_t fa_fwd_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_
   c.H_kv = static_cast<int32_t>(H_kv);
   char* ws = static_cast<char*>(workspace);
 
-  if (rows > kStreamRows) {
+  if (!streams(rows, n_seqs, total_k)) {
     const UnpackLayout l = unpack_layout(n_seqs, total_k, H_kv, D);
     UnpackParams u = {};
     u.cache = c;

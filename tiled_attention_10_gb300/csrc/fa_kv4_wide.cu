@@ -6,9 +6,13 @@
  * With few rows HBM's time for a 128-key block (784 cycles an SM) is far above
  * the products', and mma.sync straight from registers serves (fa_kv4_attn.cu).
  * From 17 rows on its products and registers cost more than that, while here a
- * block costs the same for any number of rows up to 128: 1024 cycles of
- * tcgen05 products and about 1300 of shared memory (64 KB of f16 written, read
- * once by each product, Q read again).
+ * block costs nearly the same for any number of rows up to 128.  Measured with
+ * 128 sequences of 8192 keys (H_kv 8, D 128): 512 us up to 64 rows, 536 with 128
+ * (1.02 PFLOP/s); HBM alone would take 178.  A block's 2240 cycles are the
+ * softmax warps' (one a sub-partition, some 520 instructions for a row of 128
+ * scores, beside two unpacking warps); the issue of 16 products takes 1600 of
+ * them, the unpacking 1200.  S^T = K Q^T with tiles of 64 rows, a key a thread
+ * and K's tiles in tensor memory: 517 us, and twice that for 128 rows.
  *
  * One block a SM, sixteen warps:
  *   warps 0-3   one query row a thread: Q to shared memory (f16), softmax of the
@@ -67,6 +71,12 @@ __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y,
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// mbar_wait of a whole warp, with one answer: a warp that gives up does so as
+// one, before its next tcgen05 instruction.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const fa::WaitCtl& c) {
+  return __all_sync(0xffffffffu, fa::mbar_wait(bar, parity, c));
+}
 
 // One key row's codes and scales.
 template <int D>
@@ -180,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
       bool ok = true;
       for (uint32_t j = 0; j < n; ++j) {
         const uint32_t at = done + j, slot = at & 1;
-        if (!fa::mbar_wait(bar(kSFull + slot), (at >> 1) & 1, wc)) { ok = false; break; }
+        if (!warp_wait(bar(kSFull + slot), (at >> 1) & 1, wc)) { ok = false; break; }
         if (active) {
           fa::tc_fence_after();
           const uint32_t tS = tmem + lanes + kTmemS + slot * 128;
@@ -213,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
             m = to;
             l *= a;
             if (j > 0) {
-              if (!fa::mbar_wait(bar(kODone), (at - 1) & 1, wc)) ok = false;
+              if (!warp_wait(bar(kODone), (at - 1) & 1, wc)) ok = false;
               fa::tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
@@ -254,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
       // ---- output
       if (ok && active) {
         if (n > 0) {
-          ok = fa::mbar_wait(bar(kODone), (done + n - 1) & 1, wc);
+          ok = warp_wait(bar(kODone), (done + n - 1) & 1, wc);
           fa::tc_fence_after();
         }
         const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
@@ -365,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
       bool ok = true;
       auto step = [&](uint32_t j, KeyRow<D>& k) {
         const uint32_t at = done + j, slot = at & 1;
-        if (!fa::mbar_wait(bar(empty + slot), ((at >> 1) & 1) ^ 1u, wc)) { ok = false; return; }
+        if (!warp_wait(bar(empty + slot), ((at >> 1) & 1) ^ 1u, wc)) { ok = false; return; }
         put(k, tiles + slot * C::kTile);
         fetch(j + 2, page, k);
         page = page_of(j + 3);
@@ -396,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
         for (uint32_t j = 0; j <= n && ok; ++j) {
           if (j < n) {
             const uint32_t at = done + j, slot = at & 1;
-            ok = fa::mbar_wait(bar(kKFull + slot), (at >> 1) & 1, wc);
+            ok = warp_wait(bar(kKFull + slot), (at >> 1) & 1, wc);
             if (!ok) break;
             fa::tc_fence_after();
             const uint32_t k_lo = fa::umma_desc_lo(smem + C::kK + slot * C::kTile, 16);
@@ -410,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
           }
           if (j > 0) {
             const uint32_t at = done + j - 1, slot = at & 1;
-            ok = fa::mbar_wait(bar(kVFull + slot), (at >> 1) & 1, wc) && fa::mbar_wait(bar(kPFull + slot), (at >> 1) & 1, wc);
+            ok = warp_wait(bar(kVFull + slot), (at >> 1) & 1, wc) && warp_wait(bar(kPFull + slot), (at >> 1) & 1, wc);
             if (!ok) break;
             fa::tc_fence_after();
             const uint32_t v_lo = fa::umma_desc_lo(smem + C::kV + slot * C::kTile, C::kSlab);
@@ -426,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
         if (!ok) {                          // products on their way end before the memory is freed
           fa::umma_commit_if(leader, bar(kDrain));
           const fa::WaitCtl last{limit_ns, err, &drain_flag};
-          fa::mbar_wait(bar(kDrain), 0, last);
+          warp_wait(bar(kDrain), 0, last);
         }
       } else if (warp == kMmaWarp + 1 && lane == 0 && un.more && units[(turn + 1) & 3].more) {
         next_unit<kRows>(p, cursor, units[(turn + 2) & 3]);
