@@ -272,7 +272,7 @@ def test_magnitudes(cuda_lib, std, mul):
 
 
 def test_pages_outside_the_cache_read_as_zeros(cuda_lib):
-    for qn in (1, 40):
+    for qn in (1, 12, 40, 100):
         st = Step([qn, qn], [100, 70], 4, 2, 128, 16, "bf16", seed=6, bad_page=True)
         st.check(*st.run())
 
@@ -358,7 +358,7 @@ def test_cache_past_32_bit_offsets(cuda_lib):
     sk, sv = fa.kv4_read(small, torch.arange(50, device="cuda"))
     assert torch.equal(rk, sk) and torch.equal(rv, sv)
     used = torch.tensor([50], dtype=torch.int32, device="cuda")
-    for n in (1, 50):
+    for n in (1, 4, 10, 50):
         q = torch.randn(n, 4, 128, generator=g).bfloat16().cuda()
         cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
         a = fa.paged_attention_kv4(q, c, cu, used, table.cuda(), max_seqlen_q=n, total_k=50)

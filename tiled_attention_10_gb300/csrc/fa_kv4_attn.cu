@@ -677,11 +677,12 @@ __global__ void __launch_bounds__(kUnpackThreads) fa_kv4_unpack_kernel(const __g
 // mma.sync operands, up to which it is unpacked on the way to tcgen05, and up to
 // which it is so where the sequences are long (total_k a sequence): a workspace
 // of 16-bit rows costs what it writes and reads, a 128-row tile its unpacking.
-// us, tiles / workspace, D 128, H 32 / 8: 128 sequences of 8192 keys 32 rows 512
-// (508 in mma.sync operands), 64 rows 513, 128 rows 536 / 1450, 256 rows
-// 1040 / 1600, 512 rows 2050 / 2300; 32 of 2048 256 rows 110 / 132, 512 rows
-// 187 / 195; 8 of 2048 256 rows 49 / 47, 512 rows 68 / 52; one of 65536 256
-// rows 107 / 690; 256 of 256 256 rows 248 / 165.
+// us, tiles / workspace, D 128, H 32 / 8: 128 sequences of 8192 keys 32 rows 449
+// (506 in mma.sync operands), 64 rows 455, 128 rows 479 / 1554, 256 rows
+// 920 / 1600, 512 rows 1833 / 2298; 32 of 2048 256 rows 104 / 132, 512 rows
+// 173 / 195; 8 of 2048 256 rows 48 / 47, 512 rows 66 / 52; one of 65536 256
+// rows 100 / 690, 512 rows 142 / 699; 256 of 256 128 rows 133 / 152, 256 rows
+// 239 / 165.
 constexpr int64_t kNarrowRows = 16, kStreamRows = 128, kLongStreamRows = 512, kLongKeys = 2048;
 bool streams(int64_t rows, int64_t n_seqs, int64_t total_k) {
   return rows <= (total_k / kLongKeys >= n_seqs ? kLongStreamRows : kStreamRows);

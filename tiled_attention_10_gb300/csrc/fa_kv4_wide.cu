@@ -7,12 +7,16 @@
  * the products', and mma.sync straight from registers serves (fa_kv4_attn.cu).
  * From 17 rows on its products and registers cost more than that, while here a
  * block costs nearly the same for any number of rows up to 128.  Measured with
- * 128 sequences of 8192 keys (H_kv 8, D 128): 512 us up to 64 rows, 536 with 128
- * (1.02 PFLOP/s); HBM alone would take 178.  A block's 2240 cycles are the
- * softmax warps' (one a sub-partition, some 520 instructions for a row of 128
- * scores, beside two unpacking warps); the issue of 16 products takes 1600 of
- * them, the unpacking 1200.  S^T = K Q^T with tiles of 64 rows, a key a thread
- * and K's tiles in tensor memory: 517 us, and twice that for 128 rows.
+ * 128 sequences of 8192 keys (H_kv 8, D 128): 449 us with 32 rows, 479 with 128
+ * (1.15 PFLOP/s); HBM alone would take 178.  A block takes 2000 cycles: the
+ * softmax warps (one a sub-partition, a row of 128 scores a thread) are busy all
+ * of them, the issue of the 16 products and its waits about 1600, an unpacking
+ * warp about 1100.  In pairs of fp32 (f32x2) the softmax took the kernel from
+ * 512 us to 460; a page looked up without a branch around it, 450.  Tried and
+ * slower: P against the maximum so far with a check behind it (550), two softmax
+ * warpgroups on alternate blocks with unpacking from a cp.async ring (510),
+ * S^T = K Q^T with tiles of 64 rows and K's tiles in tensor memory (510, and
+ * twice that for 128 rows).
  *
  * One block a SM, sixteen warps:
  *   warps 0-3   one query row a thread: Q to shared memory (f16), softmax of the
@@ -174,7 +178,6 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
         st_shared_v4(smem + C::kQ + tile_at(r, i), q[4 * i] ^ flip, q[4 * i + 1] ^ flip, q[4 * i + 2] ^ flip, q[4 * i + 3] ^ flip);
-      fence_async_smem();
       asm volatile("bar.sync 1, 160;" ::: "memory");        // Q is there: the issuing warp joins
 
       // ---- softmax
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
           const int key0 = key_begin + static_cast<int>(j) * kBlockKeys;
           const int lim = limit - key0;                      // columns this row sees
           const bool edge = __any_sync(0xffffffffu, lim < kBlockKeys);
-          float top = -CUDART_INF_F;
+          float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
           uint32_t v[4][32];
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld_x32(tS + c * 32, v[c]);
@@ -215,8 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int i = 0; i < 32; i += 2)
-              top = fa::max3(top, __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
-          top *= sl2;
+              tops[c] = fa::max3(tops[c], __uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
+          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * sl2;
           if (__any_sync(0xffffffffu, top > m + kLag)) {     // move the maximum: rescale O
             const float to = fmaxf(m, top);
             const float a = to == -CUDART_INF_F ? 1.0f : fa::ex2(m - to);
@@ -238,22 +241,26 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
             }
           }
           const float sub = m == -CUDART_INF_F ? 0.0f : kBias - m;
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          const uint64_t sl2s = fa::f2_pack(sl2, sl2), subs = fa::f2_pack(sub, sub);
+          uint64_t sum[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t pk[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const int e = c * 64 + 2 * i;
-              const float x = fa::ex2(fmaf(__uint_as_float(v[e / 32][e % 32]), sl2, sub));
-              const float y = fa::ex2(fmaf(__uint_as_float(v[e / 32][e % 32 + 1]), sl2, sub));
-              sum[i & 1] += x;
-              sum[2 + (i & 1)] += y;
+              float x, y;
+              fa::f2_unpack(fa::f2_fma(fa::f2_pack(__uint_as_float(v[e / 32][e % 32]), __uint_as_float(v[e / 32][e % 32 + 1])), sl2s, subs), x, y);
+              x = fa::ex2(x);
+              y = fa::ex2(y);
+              sum[i & 3] = fa::f2_add(sum[i & 3], fa::f2_pack(x, y));
               pk[i] = pack_half(x, y);
             }
             tmem_st_x32(tS + c * 32, pk);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          float x, y;
+          fa::f2_unpack(fa::f2_add(fa::f2_add(sum[0], sum[1]), fa::f2_add(sum[2], sum[3])), x, y);
+          l += x + y;
           fa::tmem_wait_st();
           fa::tc_fence_before();
         }
@@ -330,19 +337,21 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
       const uint32_t tiles = smem + (which ? C::kV : C::kK);
       const uint32_t table = static_cast<uint32_t>(un.s) * static_cast<uint32_t>(p.max_pages);
       const int ps = p.cache.page_size;
-      auto page_of = [&](uint32_t j) -> int {      // the page of block j's key, or -1
-        const int key = key_begin + static_cast<int>(j) * kBlockKeys + r;
-        if (j >= n || key >= key_end) return -1;
-        return p.block_table[table + (p.page_shift >= 0 ? key >> p.page_shift : key / ps)];
+      // A step's page is looked up before it is known whether the step is there
+      // (of the unit's last key then): no branch, so nothing waits for the page.
+      auto key_of = [&](uint32_t j) { return key_begin + static_cast<int>(j) * kBlockKeys + r; };
+      auto page_of = [&](uint32_t j) {
+        const int key = max(min(key_of(j), key_end - 1), 0);
+        return __ldg(p.block_table + (table + (p.page_shift >= 0 ? key >> p.page_shift : key / ps)));
       };
       auto fetch = [&](uint32_t j, int page, KeyRow<D>& k) {
+        const int key = key_of(j);
+        const int in_page = p.page_shift >= 0 ? key & (ps - 1) : key % ps;
+        const uint32_t at = (static_cast<uint32_t>(page) * p.cache.H_kv + head) * ps + in_page;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) k.codes[i] = make_uint4(0u, 0u, 0u, 0u);
         k.scales = make_uint2(0u, 0u);
-        if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.cache.num_pages)) {
-          const int key = key_begin + static_cast<int>(j) * kBlockKeys + r;
-          const int in_page = p.page_shift >= 0 ? key & (ps - 1) : key % ps;
-          const uint32_t at = (static_cast<uint32_t>(page) * p.cache.H_kv + head) * ps + in_page;
+        if (key < key_end && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.cache.num_pages)) {
           const uint4* c = reinterpret_cast<const uint4*>(p.cache.codes[which] + static_cast<uint64_t>(at) * (D / 2));
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) k.codes[i] = __ldg(c + i);
@@ -379,7 +388,6 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
         put(k, tiles + slot * C::kTile);
         fetch(j + 2, page, k);
         page = page_of(j + 3);
-        fence_async_smem();
         __syncwarp();
         if (lane == 0) fa::mbar_arrive(bar(full + slot));
       };
@@ -403,11 +411,13 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
       if (warp == kMmaWarp) {
         // ---- products
         asm volatile("bar.sync 1, 160;" ::: "memory");        // Q
+        fence_async_smem();
         for (uint32_t j = 0; j <= n && ok; ++j) {
           if (j < n) {
             const uint32_t at = done + j, slot = at & 1;
             ok = warp_wait(bar(kKFull + slot), (at >> 1) & 1, wc);
             if (!ok) break;
+            fence_async_smem();
             fa::tc_fence_after();
             const uint32_t k_lo = fa::umma_desc_lo(smem + C::kK + slot * C::kTile, 16);
   #pragma unroll
@@ -422,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
             const uint32_t at = done + j - 1, slot = at & 1;
             ok = warp_wait(bar(kVFull + slot), (at >> 1) & 1, wc) && warp_wait(bar(kPFull + slot), (at >> 1) & 1, wc);
             if (!ok) break;
+            fence_async_smem();
             fa::tc_fence_after();
             const uint32_t v_lo = fa::umma_desc_lo(smem + C::kV + slot * C::kTile, C::kSlab);
   #pragma unroll
@@ -435,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
         }
         if (!ok) {                          // products on their way end before the memory is freed
           fa::umma_commit_if(leader, bar(kDrain));
-          const fa::WaitCtl last{limit_ns, err, &drain_flag};
+          const fa::WaitCtl last{limit_ns > 1000000u ? limit_ns : 1000000u, err, &drain_flag};
           warp_wait(bar(kDrain), 0, last);
         }
       } else if (warp == kMmaWarp + 1 && lane == 0 && un.more && units[(turn + 1) & 3].more) {
