@@ -270,10 +270,10 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
 
       // ---- output
       if (ok && active) {
-        if (n > 0) {
-          ok = warp_wait(bar(kODone), (done + n - 1) & 1, wc);
-          fa::tc_fence_after();
-        }
+        // (the last S came after the product two blocks before it only: the one
+        // between has to be waited for too, or its phase be taken for the last)
+        for (uint32_t b = n > 2 ? n - 2 : 0; b < n; ++b) ok = warp_wait(bar(kODone), (done + b) & 1, wc) && ok;
+        fa::tc_fence_after();
         const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
         const float lse = l == 0.0f ? -CUDART_INF_F : (m - kBias + log2f(l)) * 0.69314718055994530942f;
         const bool whole = un.piece < 0;
