@@ -63,8 +63,9 @@ struct WideCfg {
 };
 
 // Barriers, each a phase an event: K / V buffer written, K / V buffer read, S
-// ready, P ready (per buffer), O updated.
-enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kODone = 12, kDrain = 13, kBarriers = 14 };
+// ready, P ready, O updated with P and V of a buffer (all per buffer: a phase
+// two blocks old is over when a block's S is there, one block old it need not be).
+enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kODone = 12, kDrain = 14, kBarriers = 15 };
 
 // Byte of element piece `piece` (8 elements of 16 bits) of row r in a tile of
 // 128-byte rows, 128-byte swizzle, 64 elements a slab.
@@ -110,8 +111,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
       fa::mbar_init(bar(kVEmpty + s), 1);
       fa::mbar_init(bar(kSFull + s), 1);
       fa::mbar_init(bar(kPFull + s), kSoftmaxWarps);
+      fa::mbar_init(bar(kODone + s), 1);
     }
-    fa::mbar_init(bar(kODone), 1);
     fa::mbar_init(bar(kDrain), 1);
     abort_flag = drain_flag = 0;
     fa::fence_mbar_init();
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
             m = to;
             l *= a;
             if (j > 0) {
-              if (!warp_wait(bar(kODone), (at - 1) & 1, wc)) ok = false;
+              if (!warp_wait(bar(kODone + (slot ^ 1u)), ((at - 1) >> 1) & 1, wc)) ok = false;
               fa::tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
@@ -270,9 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
 
       // ---- output
       if (ok && active) {
-        // (the last S came after the product two blocks before it only: the one
-        // between has to be waited for too, or its phase be taken for the last)
-        for (uint32_t b = n > 2 ? n - 2 : 0; b < n; ++b) ok = warp_wait(bar(kODone), (done + b) & 1, wc) && ok;
+        // the last block of each buffer
+        for (uint32_t b = n > 2 ? n - 2 : 0; b < n; ++b) ok = warp_wait(bar(kODone + ((done + b) & 1)), ((done + b) >> 1) & 1, wc) && ok;
         fa::tc_fence_after();
         const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
         const float lse = l == 0.0f ? -CUDART_INF_F : (m - kBias + log2f(l)) * 0.69314718055994530942f;
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
                 fa::umma_ts_w<false>(tmem + kTmemO, tmem + kTmemS + slot * 128 + kk * 8, v_lo + static_cast<uint32_t>((kk * 16 * 128) >> 4), hi,
                                      C::kIdescPV, j > 1 || kk > 0);
             fa::umma_commit_if(leader, bar(kVEmpty + slot));
-            fa::umma_commit_if(leader, bar(kODone));
+            fa::umma_commit_if(leader, bar(kODone + slot));
           }
         }
         if (!ok) {                          // products on their way end before the memory is freed
