@@ -14,7 +14,8 @@
  * warp about 1100.  In pairs of fp32 (f32x2) the softmax took the kernel from
  * 512 us to 460; a page looked up without a branch around it, 450.  Tried and
  * slower: P against the maximum so far with a check behind it (550), two softmax
- * warpgroups on alternate blocks with unpacking from a cp.async ring (510),
+ * warpgroups, on alternate blocks (487) or on half of each block's keys (457, 501
+ * with 128 rows; faster at D = 64, 702 for 256 sequences against 788),
  * S^T = K Q^T with tiles of 64 rows and K's tiles in tensor memory (510, and
  * twice that for 128 rows).
  *
@@ -50,6 +51,7 @@ constexpr int kThreads = (kMmaWarp + 4) * 32;
 // Registers a thread, of 512 for the four warpgroups.
 constexpr int kSoftmaxRegs = 216, kUnpackRegs = 104, kOtherRegs = 88;
 static_assert(kSoftmaxRegs + 2 * kUnpackRegs + kOtherRegs <= 4 * 128, "more than the launch has");
+static_assert(kSoftmaxRegs >= 128 && kUnpackRegs <= 128 && kOtherRegs <= 128, "an increase has to be one, a decrease too");
 constexpr uint32_t kTmemS = 0, kTmemO = 256;
 
 template <int D>
