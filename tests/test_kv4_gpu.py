@@ -330,6 +330,23 @@ def test_two_streams_at_once(cuda_lib):
             assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("qn", [1, 4, 9, 100])
+def test_captured_over_changing_lengths(cuda_lib, qn):
+    """One graph, replayed as the lengths and queries change, against calls made one by one."""
+    st = Step([qn] * 3, [700, 130, 1000], 8, 2, 128, 32, "bf16", seed=24)
+    ws = fa.paged_attention_kv4_workspace(st.q, st.cache, max_seqlen_q=qn, n_seqs=3, total_k=1830)
+    o, lse = st.run(workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fa.paged_attention_kv4(st.q, st.cache, st.cu, st.used, st.table, max_seqlen_q=qn, total_k=1830, causal=2, out=o, lse=lse, workspace=ws)
+    for used in ([700, 130, 1000], [128, 129, 0], [1, 0, 999]):
+        st.used.copy_(torch.tensor(used, dtype=torch.int32))
+        st.q.mul_(-1.0)
+        want = st.run()
+        graph.replay()
+        assert torch.equal(o.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
+
+
 def test_a_nan_query_stays_in_its_row(cuda_lib):
     for qn in (1, 4, 20, 80):
         st = Step([qn, qn], [300, 200], 8, 2, 128, 16, "bf16", seed=22)
