@@ -538,8 +538,9 @@ fa_status_t fa_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales, const u
  *   rows; keys past it may be left out).  At most 16384 sequences when
  *   unpacking.
  *   workspace: at least fa_fwd_paged_kv4_workspace_size bytes, 256-byte
- *   aligned, contents irrelevant.  Two launches; calls sharing a workspace
- *   must not overlap.  Deterministic (no atomics).  From 17 rows on the
+ *   aligned, contents irrelevant; one of that size serves any call with at
+ *   most as many sequences, queries and keys.  Two launches; calls sharing a
+ *   workspace must not overlap.  Deterministic (no atomics).  From 17 rows on the
  *   kernel's waits are bounded as the forward's are (fa_last_device_error).
  */
 fa_status_t fa_fwd_paged_kv4_workspace_size(int64_t n_seqs, int64_t max_seqlen_q, int64_t total_k,

@@ -330,6 +330,17 @@ def test_two_streams_at_once(cuda_lib):
             assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
 
 
+def test_one_workspace_for_many_steps(cuda_lib):
+    """A workspace of the largest step serves steps with fewer queries and keys, whichever way they go."""
+    big = Step([128] * 3, [2500, 2000, 2100], 8, 2, 64, 32, "bf16", seed=25)
+    ws = fa.paged_attention_kv4_workspace(big.q, big.cache, max_seqlen_q=128, n_seqs=3, total_k=6600)
+    ws.fill_(0xFF)
+    big.check(*big.run(workspace=ws), unpacked=False)
+    for qn in (1, 4, 9, 40, 128):
+        st = Step([qn] * 3, [300, 200, 100], 8, 2, 64, 32, "bf16", seed=qn)
+        st.check(*st.run(workspace=ws))
+
+
 @pytest.mark.parametrize("qn", [1, 4, 9, 100])
 def test_captured_over_changing_lengths(cuda_lib, qn):
     """One graph, replayed as the lengths and queries change, against calls made one by one."""

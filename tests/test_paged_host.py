@@ -160,6 +160,18 @@ def test_attention_workspace(built_lib):
     assert size(1, 1, 1, 8, 2, 96)[0] == 2
 
 
+def test_attention_workspace_serves_smaller_steps(built_lib):
+    """What a step needs is never more than what one with more sequences, queries or keys is told."""
+    size = lambda n, q, k, G, D: binding.fa_fwd_paged_kv4_workspace_size(n, q, k, 2 * G, 2, D)
+    ns, qs, ks = (1, 7, 64, 5000), (1, 2, 5, 16, 17, 64, 128, 129, 512, 4096), (0, 100, 2047, 2048, 20000, 131071, 131072, 1 << 24)
+    for G, D in ((1, 64), (4, 128), (7, 128)):
+        table = {(n, q, k): size(n, q, k, G, D) for n in ns for q in qs for k in ks}
+        assert all(st == 0 for st, _ in table.values())
+        for (n, q, k), (_, big) in table.items():
+            for a, b, c in ((n2, q2, k2) for n2 in ns for q2 in qs for k2 in ks if n2 <= n and q2 <= q and k2 <= k):
+                assert table[a, b, c][1] <= big, ((a, b, c), (n, q, k))
+
+
 # ---------------------------------------------------------------- torch-level checks (CPU tensors are refused)
 def test_wrappers_refuse_cpu_tensors_and_wrong_types(built_lib):
     import tiled_attention_10_gb300 as fa

@@ -782,8 +782,13 @@ fa_status_t fa_fwd_paged_kv4_workspace_size(int64_t n_seqs, int64_t max_seqlen_q
   if (max_seqlen_q > kMaxRows || total_k > kMaxRows || H > 65536 || n_seqs > INT32_MAX - 1)
     return FA_ERR_UNSUPPORTED;
   const int64_t rows = max_seqlen_q * (H / H_kv);
-  *workspace_bytes = streams(rows, n_seqs, total_k) ? stream_layout(D, tiles_for(rows)).bytes
-                                                    : unpack_layout(n_seqs, total_k, H_kv, D).bytes;
+  // What a step with fewer sequences, queries or keys needs too: the layouts of
+  // fewer rows, and unpacked keys where only their number keeps this one from it.
+  *workspace_bytes = stream_layout(D, tiles_for(rows)).bytes;
+  if (rows > kStreamRows) {
+    const int64_t keys = rows > kLongStreamRows ? total_k : std::min(total_k, kLongKeys * n_seqs);
+    *workspace_bytes = std::max(*workspace_bytes, unpack_layout(n_seqs, keys, H_kv, D).bytes);
+  }
   return FA_OK;
 }
 

@@ -261,7 +261,7 @@ def paged_attention_kv4(q, cache, cu_seqlens_q, seqused_k, block_table, *, max_s
     elif not _is(lse, torch.float32, (H, total_q), index):
         _check("lse", lse, torch.float32, (H, total_q), index)
     if total_k is None:
-        total_k = n * max_pages * rows
+        total_k = min(n * max_pages * rows, (1 << 31) - 256)   # (the most a call takes; short queries do not need it)
     if workspace is None:
         workspace = paged_attention_kv4_workspace(q, cache, max_seqlen_q=max_seqlen_q, n_seqs=n, total_k=total_k)
     elif workspace.dim() != 1 or not _is(workspace, _U8, workspace.shape, index):
