@@ -330,6 +330,21 @@ def test_two_streams_at_once(cuda_lib):
             assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
 
 
+def test_a_wide_table_needs_no_total_k(cuda_lib):
+    """More places in the block table than keys a call may count, with one query each."""
+    st = Step([1, 1], [70, 130], 4, 2, 64, 64, "bf16", seed=26)
+    st.check(*st.run())
+    n = 4100
+    table = torch.full((n, 8192), -1, dtype=torch.int32, device="cuda")
+    table[:2, :st.table.shape[1]] = st.table
+    used = torch.zeros(n, dtype=torch.int32, device="cuda")
+    used[:2] = st.used
+    cu = torch.full((n + 1,), 2, dtype=torch.int32, device="cuda")
+    cu[:2] = torch.arange(2, device="cuda")
+    a, b = st.run(), fa.paged_attention_kv4(st.q, st.cache, cu, used, table, max_seqlen_q=1)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_one_workspace_for_many_steps(cuda_lib):
     """A workspace of the largest step serves steps with fewer queries and keys, whichever way they go."""
     big = Step([128] * 3, [2500, 2000, 2100], 8, 2, 64, 32, "bf16", seed=25)
