@@ -12,7 +12,10 @@
  * softmax warps (one a sub-partition, a row of 128 scores a thread) are busy all
  * of them, the issue of the 16 products and its waits about 1600, an unpacking
  * warp about 1100.  In pairs of fp32 (f32x2) the softmax took the kernel from
- * 512 us to 460; a page looked up without a branch around it, 450.  Tried and
+ * 512 us to 460; a page looked up without a branch around it, 450; the next
+ * unit's first rows loaded while a unit ends, 336 us for 1000 sequences of 256
+ * keys instead of 346 (12,000 cycles a unit of two blocks, most of them one
+ * latency after another: Q, S, softmax twice, output).  Tried and
  * slower: P against the maximum so far with a check behind it (550), two softmax
  * warpgroups, on alternate blocks (487) or on half of each block's keys (457, 501
  * with 128 rows; faster at D = 64, 702 for 256 sequences against 788),
@@ -327,62 +330,70 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
       if (!next(ok, un.more)) break;
     }
   } else if (warp < kMmaWarp) {
+    // ---- unpack: this lane's key row of each block, of K or of V
     fa::reg_alloc_dec<kUnpackRegs>();
-    for (int turn = 0;; turn = (turn + 1) & 3) {
-      const Unit& un = units[turn];
-      const int key_begin = un.key_begin, key_end = un.key_end, head = un.head;
-      const uint32_t n = static_cast<uint32_t>((key_end - key_begin + kBlockKeys - 1) / kBlockKeys);
-      // ---- unpack: this lane's key row of each block, of K or of V
-      const int which = warp >= kSoftmaxWarps + kUnpackWarps;
-      const int r = (warp - kSoftmaxWarps - which * kUnpackWarps) * 32 + lane;
-      const int full = which ? kVFull : kKFull, empty = which ? kVEmpty : kKEmpty;
-      const uint32_t tiles = smem + (which ? C::kV : C::kK);
-      const uint32_t table = static_cast<uint32_t>(un.s) * static_cast<uint32_t>(p.max_pages);
-      const int ps = p.cache.page_size;
-      // A step's page is looked up before it is known whether the step is there
-      // (of the unit's last key then): no branch, so nothing waits for the page.
-      auto key_of = [&](uint32_t j) { return key_begin + static_cast<int>(j) * kBlockKeys + r; };
-      auto page_of = [&](uint32_t j) {
-        const int key = max(min(key_of(j), key_end - 1), 0);
-        return __ldg(p.block_table + (table + (p.page_shift >= 0 ? key >> p.page_shift : key / ps)));
-      };
-      auto fetch = [&](uint32_t j, int page, KeyRow<D>& k) {
-        const int key = key_of(j);
-        const int in_page = p.page_shift >= 0 ? key & (ps - 1) : key % ps;
-        const uint32_t at = (static_cast<uint32_t>(page) * p.cache.H_kv + head) * ps + in_page;
+    const int which = warp >= kSoftmaxWarps + kUnpackWarps;
+    const int r = (warp - kSoftmaxWarps - which * kUnpackWarps) * 32 + lane;
+    const int full = which ? kVFull : kKFull, empty = which ? kVEmpty : kKEmpty;
+    const uint32_t tiles = smem + (which ? C::kV : C::kK);
+    const int ps = p.cache.page_size;
+    int key_begin, key_end, head;           // of the unit being loaded
+    uint32_t n, table;
+    // A step's page is looked up before it is known whether the step is there
+    // (of the unit's last key then): no branch, so nothing waits for the page.
+    auto key_of = [&](uint32_t j) { return key_begin + static_cast<int>(j) * kBlockKeys + r; };
+    auto page_of = [&](uint32_t j) {
+      const int key = max(min(key_of(j), key_end - 1), 0);
+      return __ldg(p.block_table + (table + (p.page_shift >= 0 ? key >> p.page_shift : key / ps)));
+    };
+    auto fetch = [&](uint32_t j, int page, KeyRow<D>& k) {
+      const int key = key_of(j);
+      const int in_page = p.page_shift >= 0 ? key & (ps - 1) : key % ps;
+      const uint32_t at = (static_cast<uint32_t>(page) * p.cache.H_kv + head) * ps + in_page;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) k.codes[i] = make_uint4(0u, 0u, 0u, 0u);
-        k.scales = make_uint2(0u, 0u);
-        if (key < key_end && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.cache.num_pages)) {
-          const uint4* c = reinterpret_cast<const uint4*>(p.cache.codes[which] + static_cast<uint64_t>(at) * (D / 2));
+      for (int i = 0; i < D / 32; ++i) k.codes[i] = make_uint4(0u, 0u, 0u, 0u);
+      k.scales = make_uint2(0u, 0u);
+      if (key < key_end && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.cache.num_pages)) {
+        const uint4* c = reinterpret_cast<const uint4*>(p.cache.codes[which] + static_cast<uint64_t>(at) * (D / 2));
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) k.codes[i] = __ldg(c + i);
-          const uint8_t* s = p.cache.scales[which] + static_cast<uint64_t>(at) * (D / 16);
-          if (D == 128) k.scales = __ldg(reinterpret_cast<const uint2*>(s));
-          else k.scales.x = __ldg(reinterpret_cast<const uint32_t*>(s));
+        for (int i = 0; i < D / 32; ++i) k.codes[i] = __ldg(c + i);
+        const uint8_t* s = p.cache.scales[which] + static_cast<uint64_t>(at) * (D / 16);
+        if (D == 128) k.scales = __ldg(reinterpret_cast<const uint2*>(s));
+        else k.scales.x = __ldg(reinterpret_cast<const uint32_t*>(s));
+      }
+    };
+    auto put = [&](const KeyRow<D>& k, uint32_t tile) {
+      const uint32_t scale[2] = {k.scales.x, k.scales.y};
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t w[4] = {k.codes[i].x, k.codes[i].y, k.codes[i].z, k.codes[i].w};
+        const uint32_t two = scales_to_half((scale[i / 2] >> (16 * (i % 2))) & 0xffffu);   // of 32 elements
+        const uint32_t s2[2] = {__byte_perm(two, 0u, 0x1010), __byte_perm(two, 0u, 0x3232)};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t h[4];
+          codes_to_half(w[x], h);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) h[y] = mul_half(h[y], s2[x / 2]);
+          st_shared_v4(tile + tile_at(r, 4 * i + x), h[0], h[1], h[2], h[3]);
         }
-      };
-      auto put = [&](const KeyRow<D>& k, uint32_t tile) {
-        const uint32_t scale[2] = {k.scales.x, k.scales.y};
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint32_t w[4] = {k.codes[i].x, k.codes[i].y, k.codes[i].z, k.codes[i].w};
-          const uint32_t two = scales_to_half((scale[i / 2] >> (16 * (i % 2))) & 0xffffu);   // of 32 elements
-          const uint32_t s2[2] = {__byte_perm(two, 0u, 0x1010), __byte_perm(two, 0u, 0x3232)};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t h[4];
-            codes_to_half(w[x], h);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) h[y] = mul_half(h[y], s2[x / 2]);
-            st_shared_v4(tile + tile_at(r, 4 * i + x), h[0], h[1], h[2], h[3]);
-          }
-        }
-      };
-      KeyRow<D> ring[2];
+      }
+    };
+    KeyRow<D> ring[2];
+    int page;
+    // A unit's first two blocks on their way: while the unit before it ends.
+    auto begin = [&](const Unit& un) {
+      key_begin = un.key_begin;
+      key_end = un.key_end;
+      head = un.head;
+      n = static_cast<uint32_t>((key_end - key_begin + kBlockKeys - 1) / kBlockKeys);
+      table = static_cast<uint32_t>(un.s) * static_cast<uint32_t>(p.max_pages);
       fetch(0, page_of(0), ring[0]);
       fetch(1, page_of(1), ring[1]);
-      int page = page_of(2);
+      page = page_of(2);
+    };
+    begin(units[0]);
+    for (int turn = 0;; turn = (turn + 1) & 3) {
       bool ok = true;
       auto step = [&](uint32_t j, KeyRow<D>& k) {
         const uint32_t at = done + j, slot = at & 1;
@@ -398,7 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
         if (j + 1 < n && ok) step(j + 1, ring[1]);
       }
       done += n;                            // all phases follow the blocks before this unit
-      if (!next(ok, un.more)) break;
+      const bool more = units[turn].more;
+      if (more) begin(units[(turn + 1) & 3]);
+      if (!next(ok, more)) break;
     }
   } else {
     fa::reg_alloc_dec<kOtherRegs>();
