@@ -29,8 +29,7 @@
  *               128-key blocks ahead, written as f16 in the 128-byte swizzle
  *   warp  12    issues S(j) = Q K_j^T and then O += P(j-1) V_(j-1)
  *   warp  13    finds the unit after the next
- * (the last four get the registers that a thread of the softmax, with a row of
- * S, needs beyond its share).
+ * (warps 4-15 give up registers to the softmax's, whose threads hold a row of S).
  * Tensor memory: S in two buffers of 128 columns (P overwrites the first half
  * of its own), O in 128.  Rounding as in fa_kv4_attn.cu: P in f16 only.
  * The units come from the same even split of the work, with the same merge.
