@@ -170,10 +170,11 @@ def _to_cache(x, descale):
     the inputs are 16-bit values, so that many lie next to a border or on it."""
     shape = x.shape
     x = x.reshape(-1, shape[-1] // 16, 16).double()
-    want = x.abs().amax(-1) / (6.0 * descale)
+    g = descale.double()
+    want = x.abs().amax(-1) / (6.0 * g)
     step = torch.exp2((torch.frexp(want)[1] - 1).clamp_(min=-6).double() - 3.0)
     scale = (torch.round(want / step) * step).clamp_(max=448.0)
-    y = torch.where((scale > 0).unsqueeze(-1), x / (scale * descale).unsqueeze(-1), torch.zeros_like(x))
+    y = torch.where((scale > 0).unsqueeze(-1), x / (scale * g).unsqueeze(-1), torch.zeros_like(x))
     a = y.abs()
     code = ((a > 0.25).to(torch.uint8) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0)).to(torch.uint8)
     code = code + torch.signbit(y).to(torch.uint8) * 8
@@ -197,7 +198,7 @@ def _make_cache(pages, c, g, fill):
         codes = torch.zeros(*shape[:-1], c["D"] // 2, dtype=torch.uint8, device="cuda")
         scales = torch.zeros(*shape[:-1], c["D"] // 16, dtype=torch.float8_e4m3fn, device="cuda")
         # the descale that puts the largest values in the e4m3 scale's upper range
-        descale = torch.tensor(6.5 * std / (6.0 * 448.0), dtype=torch.float32).item()
+        descale = torch.tensor([6.5 * std / (6.0 * 448.0)], dtype=torch.float32, device="cuda")
         if fill:
             per = max(1, (1 << 25) // math.prod(shape[1:]))
             for a in range(0, pages, per):
@@ -493,7 +494,7 @@ def exact(case, seed):
         grid = torch.tensor(E2M1, dtype=torch.float64, device="cuda")
         for x, name in ((s["k"], "k"), (s["v"], "v")):
             x = x.double()
-            g = s[name + "_descale"]
+            g = s[name + "_descale"].double()
             y = x.reshape(*x.shape[:-1], -1, 16)
             want = y.abs().amax(-1) / (6.0 * g)
             # the nearest e4m3 value: 3 mantissa bits above 2^-6, steps of 2^-9 below
@@ -517,8 +518,8 @@ def exact(case, seed):
         rows = torch.arange(at, at + ql, device="cuda")
         last = kl - ql + torch.arange(ql, device="cuda")
         for j in range(hk):
-            k = _decode64(s["k_codes"][pages, j], s["k_scales"].view(torch.uint8)[pages, j]).reshape(-1, d)[:kl] * s["k_descale"]
-            v = _decode64(s["v_codes"][pages, j], s["v_scales"].view(torch.uint8)[pages, j]).reshape(-1, d)[:kl] * s["v_descale"]
+            k = _decode64(s["k_codes"][pages, j], s["k_scales"].view(torch.uint8)[pages, j]).reshape(-1, d)[:kl] * s["k_descale"].double()
+            v = _decode64(s["v_codes"][pages, j], s["v_scales"].view(torch.uint8)[pages, j]).reshape(-1, d)[:kl] * s["v_descale"].double()
             for m in range(j * (h // hk), (j + 1) * (h // hk)):
                 a = s["q"][rows, m].double() @ k.t() * s["scale"]
                 a = torch.where(torch.arange(kl, device="cuda")[None, :] <= last[:, None], a, torch.full_like(a, -math.inf))
