@@ -492,7 +492,10 @@ fa_status_t fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const vo
  * fa_kv4_write never makes, reads as NaN (and may reach the neighbours of the
  * sequence that holds it); nothing else makes a value NaN or infinite.
  * descale_k, descale_v are host floats in [2^-100, 2^100] (FA_ERR_INVALID_ARG
- * outside).  D 64 or 128; codes and scales 16-byte aligned; page sizes
+ * outside).  The calls named _devscale take them as device pointers instead (one
+ * fp32 each, 4-byte aligned, NULL for 1.0) and read them when they run, so that a
+ * captured graph follows them; a value outside the range there counts as its
+ * nearer end, NaN as 2^-100.  D 64 or 128; codes and scales 16-byte aligned; page sizes
  * as fa_fwd_paged.
  *
  * fa_kv4_write -- rows of k and v into slots: row t goes to slot slot_map[t],
@@ -521,6 +524,20 @@ fa_status_t fa_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales, const u
                         float descale_k, float descale_v, int64_t n_tokens, int64_t H_kv, int64_t D,
                         int64_t page_size, int64_t num_pages, fa_dtype_t dtype,
                         cudaStream_t stream);
+
+fa_status_t fa_kv4_write_devscale(const void* k, const void* v, const int64_t* slot_map,
+                                  uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
+                                  uint8_t* v_scales, const float* descale_k, const float* descale_v,
+                                  int64_t n_tokens, int64_t H_kv, int64_t D, int64_t page_size,
+                                  int64_t num_pages, const fa_strides_t* strides, fa_dtype_t dtype,
+                                  cudaStream_t stream);
+
+fa_status_t fa_kv4_read_devscale(const uint8_t* k_codes, const uint8_t* k_scales,
+                                 const uint8_t* v_codes, const uint8_t* v_scales,
+                                 const int64_t* slot_map, void* k_out, void* v_out,
+                                 const float* descale_k, const float* descale_v, int64_t n_tokens,
+                                 int64_t H_kv, int64_t D, int64_t page_size, int64_t num_pages,
+                                 fa_dtype_t dtype, cudaStream_t stream);
 
 /*
  * fa_fwd_paged_kv4 -- attention of packed queries over the 4-bit cache: q, o,
@@ -556,6 +573,19 @@ fa_status_t fa_fwd_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_
                              int64_t D, float scale, int causal, fa_dtype_t dtype, float descale_k,
                              float descale_v, void* workspace, size_t workspace_bytes,
                              cudaStream_t stream);
+
+fa_status_t fa_fwd_paged_kv4_devscale(const void* q, const uint8_t* k_codes,
+                                      const uint8_t* k_scales, const uint8_t* v_codes,
+                                      const uint8_t* v_scales, void* o, float* lse,
+                                      const int32_t* cu_seqlens_q, const int32_t* seqused_k,
+                                      const int32_t* block_table, int64_t n_seqs,
+                                      int64_t max_pages_per_seq, int64_t page_size,
+                                      int64_t num_pages, int64_t total_q, int64_t max_seqlen_q,
+                                      int64_t total_k, int64_t H, int64_t H_kv, int64_t D,
+                                      float scale, int causal, fa_dtype_t dtype,
+                                      const float* descale_k, const float* descale_v,
+                                      void* workspace, size_t workspace_bytes,
+                                      cudaStream_t stream);
 
 /* A static, human-readable name for a status code (never NULL). */
 const char* fa_status_string(fa_status_t s);

@@ -526,3 +526,84 @@ def test_captured_decode_step(cuda_lib):
         assert torch.equal(a, o2) and torch.equal(b, l2)
         taken += int(sl2.pages_taken)
         past = sl2.seqused_k
+
+
+# ---------------------------------------------------------------- descales held on the device
+def one(x):
+    return torch.full((1,), x, dtype=torch.float32, device="cuda")
+
+
+def bits(ts):
+    return [t.clone().view(torch.uint8) for t in ts]
+
+
+def cache_bits(c):
+    return bits((c.k_codes, c.k_scales, c.v_codes, c.v_scales))
+
+
+@pytest.mark.parametrize("qn,dtype,D", [(1, "bf16", 128), (4, "f16", 64), (9, "bf16", 64), (40, "f16", 128), (100, "bf16", 128),
+                                        (100, "f16", 64)])
+def test_device_descales_give_what_floats_give(cuda_lib, qn, dtype, D):
+    """Written, read and attended to with the descales in tensors, in one of each, and as floats: bit for bit."""
+    st = Step([qn, 1], [300, 257], 8, 2, D, 16, dtype, seed=qn, kd=0.0031, vd=0.0017)
+    want = bits(st.run())
+    slots = torch.arange(64, device="cuda")
+    rows = torch.randn(64, 2, D, generator=torch.Generator().manual_seed(3)).to(DT[dtype]).cuda()
+    fa.kv4_write(rows, rows, slots, spare := junk_cache(4, 16, 2, D, 0.0031, 0.0017))
+    codes, read = cache_bits(spare), bits(fa.kv4_read(spare, slots, DT[dtype]))
+    for kd, vd in ((one(0.0031), one(0.0017)), (one(0.0031).view(()), 0.0017), (0.0031, one(0.0017))):
+        st.cache.k_descale, st.cache.v_descale = kd, vd
+        assert all(torch.equal(a, b) for a, b in zip(want, bits(st.run())))
+        c = junk_cache(4, 16, 2, D, kd, vd)
+        fa.kv4_write(rows, rows, slots, c)
+        assert all(torch.equal(a, b) for a, b in zip(codes, cache_bits(c)))
+        assert all(torch.equal(a, b) for a, b in zip(read, bits(fa.kv4_read(c, slots, DT[dtype]))))
+
+
+@pytest.mark.parametrize("qn", [1, 9, 100])
+def test_captured_calls_follow_the_device_descales(cuda_lib, qn):
+    st = Step([qn], [700], 8, 2, 128, 32, "bf16", seed=qn)
+    kd, vd = one(0.003), one(0.002)
+    st.cache.k_descale, st.cache.v_descale = kd, vd
+    rows = torch.randn(32, 2, 128, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    slots = torch.arange(32, device="cuda")
+    spare = junk_cache(1, 32, 2, 128, kd, vd)
+    ws = fa.paged_attention_kv4_workspace(st.q, st.cache, max_seqlen_q=qn, n_seqs=1, total_k=700)
+
+    def calls(cache, other):
+        fa.kv4_write(rows, rows, slots, other)
+        return (*fa.kv4_read(other, slots), *fa.paged_attention_kv4(st.q, cache, st.cu, st.used, st.table, max_seqlen_q=qn,
+                                                                    total_k=700, workspace=ws))
+
+    calls(st.cache, spare)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls(st.cache, spare)
+    for a, b in ((0.003, 0.002), (0.0007, 0.01), (0.02, 0.0001)):
+        kd.fill_(a)
+        vd.fill_(b)
+        graph.replay()
+        c = st.cache
+        fixed = fa.KV4Cache(c.k_codes, c.k_scales, c.v_codes, c.v_scales, a, b)
+        want = calls(fixed, junk_cache(1, 32, 2, 128, a, b))
+        assert all(torch.equal(x, y) for x, y in zip(bits(got), bits(want)))
+
+
+def test_device_descales_outside_the_range(cuda_lib):
+    """They count as the range's nearer end."""
+    rows = torch.randn(16, 1, 64, generator=torch.Generator().manual_seed(5)).half().cuda()
+    slots = torch.arange(16, device="cuda")
+    for bad, end in ((0.0, 2.0 ** -100), (-1.0, 2.0 ** -100), (float("nan"), 2.0 ** -100), (float("inf"), 2.0 ** 100), (1e-40, 2.0 ** -100)):
+        a, b = junk_cache(1, 16, 1, 64, one(bad), one(bad)), junk_cache(1, 16, 1, 64, end, end)
+        fa.kv4_write(rows, rows, slots, a)
+        fa.kv4_write(rows, rows, slots, b)
+        assert all(torch.equal(x, y) for x, y in zip(cache_bits(a), cache_bits(b)))
+
+
+def test_descales_of_the_wrong_kind_are_refused(cuda_lib):
+    for bad in (one(1.0).double(), one(1.0).cpu(), one(1.0).expand(2).contiguous()):
+        with pytest.raises((TypeError, ValueError)):
+            fa.KV4Cache.allocate(1, 16, 1, 64, k_descale=bad)
+        c = fa.KV4Cache.allocate(1, 16, 1, 64)
+        with pytest.raises((TypeError, ValueError)):
+            c.v_descale = bad

@@ -230,3 +230,26 @@ def test_reference_gradient_against_differences(interleaved, norm):
     if norm:
         u = g.standard_normal(64)
         assert abs((loss(x, w + e * u) - loss(x, w - e * u)) / (2 * e) - (dw * u).sum()) < 1e-6 * np.abs(dw * u).sum()
+
+
+# ---------------------------------------------------------------- descales on the device
+@pytest.mark.parametrize("over,code", [(dict(dk=P[20] + 2), 3), (dict(dv=P[21] + 1), 3), (dict(kc=None), 1),
+                                       (dict(D=96), 2), (dict(n=0, dk=None, dv=None), 0), (dict(n=0), 0)])
+def test_kv4_devscale_refusals(built_lib, over, code):
+    a = dict(KV, dk=P[20], dv=P[21], **{k: v for k, v in over.items() if k not in ("dk", "dv")})
+    a.update(over)
+    assert binding.fa_kv4_write_devscale(a["k"], a["v"], a["slot"], a["kc"], a["ks"], a["vc"], a["vs"], a["dk"], a["dv"],
+                                         a["n"], a["H_kv"], a["D"], a["ps"], a["pages"], a["st"], a["dtype"]) == code
+    assert binding.fa_kv4_read_devscale(a["kc"], a["ks"], a["vc"], a["vs"], a["slot"], a["k"], a["v"], a["dk"], a["dv"],
+                                        a["n"], a["H_kv"], a["D"], a["ps"], a["pages"], a["dtype"]) == code
+
+
+@pytest.mark.parametrize("over,code", [(dict(dk=P[20] + 2), 3), (dict(dv=P[21] + 1), 3), (dict(scale=float("nan")), 1),
+                                       (dict(D=80), 2), (dict(tq=0, dk=None, dv=None), 0), (dict(tq=0), 0)])
+def test_attention_devscale_refusals(built_lib, over, code):
+    a = dict(ATT, dk=P[20], dv=P[21])
+    a.update(over)
+    assert binding.fa_fwd_paged_kv4_devscale(
+        a["q"], a["kc"], a["ks"], a["vc"], a["vs"], a["o"], a["lse"], a["cu"], a["used"], a["table"], a["n"], a["cols"],
+        a["ps"], a["pages"], a["tq"], a["mq"], a["tk"], a["H"], a["H_kv"], a["D"], a["scale"], a["causal"], a["dtype"],
+        a["dk"], a["dv"], a["ws"], a["nbytes"]) == code

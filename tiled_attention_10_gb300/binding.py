@@ -21,7 +21,8 @@ FA_STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED",
 EXPORTS = ("fa_fwd", "fa_fwd_gqa", "fa_fwd_splitkv", "fa_fwd_splitkv_plan", "fa_fwd_splitkv_noalloc", "fa_bwd", "fa_bwd_workspace_size", "fa_fwd_varlen", "fa_fwd_paged", "fa_fwd_paged_split", "fa_fwd_paged_split_workspace_size", "fa_fwd_paged_split_plan", "fa_fwd_strided", "fa_bwd_strided", "fa_status_string", "fa_last_device_error", "fa_set_wait_limit_ns",
            "fa_probe_wait_timeout", "fa_version", "fa_paged_slots", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
            "fa_qk_norm_rope_bwd_workspace_size", "fa_kv4_write", "fa_kv4_read", "fa_fwd_paged_kv4",
-           "fa_fwd_paged_kv4_workspace_size")
+           "fa_fwd_paged_kv4_workspace_size", "fa_kv4_write_devscale", "fa_kv4_read_devscale",
+           "fa_fwd_paged_kv4_devscale")
 
 
 
@@ -125,6 +126,12 @@ def load(path: str = LIB_PATH):
     lib.fa_kv4_read.restype = ip
     lib.fa_fwd_paged_kv4.argtypes = ([vp] * 10 + [i64] * 10 + [f32, ip, ip, f32, f32, vp, sz, vp])
     lib.fa_fwd_paged_kv4.restype = ip
+    lib.fa_kv4_write_devscale.argtypes = [vp] * 9 + [i64] * 5 + [vp, ip, vp]
+    lib.fa_kv4_write_devscale.restype = ip
+    lib.fa_kv4_read_devscale.argtypes = [vp] * 9 + [i64] * 5 + [ip, vp]
+    lib.fa_kv4_read_devscale.restype = ip
+    lib.fa_fwd_paged_kv4_devscale.argtypes = ([vp] * 10 + [i64] * 10 + [f32, ip, ip, vp, vp, vp, sz, vp])
+    lib.fa_fwd_paged_kv4_devscale.restype = ip
     lib.fa_fwd_paged_kv4_workspace_size.argtypes = [i64] * 6 + [ctypes.POINTER(sz)]
     lib.fa_fwd_paged_kv4_workspace_size.restype = ip
     lib.fa_version.argtypes = []
@@ -374,6 +381,25 @@ def fa_kv4_read(k_codes, k_scales, v_codes, v_scales, slot_map, k_out, v_out, de
                                   int(D), int(page_size), int(num_pages), dt, stream))
 
 
+def fa_kv4_write_devscale(k, v, slot_map, k_codes, k_scales, v_codes, v_scales, descale_k, descale_v,
+                          n_tokens, H_kv, D, page_size, num_pages, strides, dtype, stream=None) -> int:
+    """fa_kv4_write with the descales behind device pointers (None: 1)."""
+    dt = FA_DTYPE[dtype] if isinstance(dtype, str) else int(dtype)
+    arr = None if strides is None else _strides_array(strides)
+    return int(load().fa_kv4_write_devscale(k, v, slot_map, k_codes, k_scales, v_codes, v_scales,
+                                            descale_k, descale_v, int(n_tokens), int(H_kv), int(D),
+                                            int(page_size), int(num_pages), arr, dt, stream))
+
+
+def fa_kv4_read_devscale(k_codes, k_scales, v_codes, v_scales, slot_map, k_out, v_out, descale_k,
+                         descale_v, n_tokens, H_kv, D, page_size, num_pages, dtype, stream=None) -> int:
+    """fa_kv4_read with the descales behind device pointers (None: 1)."""
+    dt = FA_DTYPE[dtype] if isinstance(dtype, str) else int(dtype)
+    return int(load().fa_kv4_read_devscale(k_codes, k_scales, v_codes, v_scales, slot_map, k_out,
+                                           v_out, descale_k, descale_v, int(n_tokens), int(H_kv),
+                                           int(D), int(page_size), int(num_pages), dt, stream))
+
+
 def fa_fwd_paged_kv4_workspace_size(n_seqs, max_seqlen_q, total_k, H, H_kv, D):
     """(status, bytes) of device workspace fa_fwd_paged_kv4 needs."""
     n = ctypes.c_size_t(0)
@@ -395,6 +421,21 @@ def fa_fwd_paged_kv4(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_q, sequ
                                        int(max_seqlen_q), int(total_k), int(H), int(H_kv), int(D),
                                        float(scale), c, dt, float(descale_k), float(descale_v),
                                        workspace, int(workspace_bytes), stream))
+
+
+def fa_fwd_paged_kv4_devscale(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_q, seqused_k,
+                              block_table, n_seqs, max_pages, page_size, num_pages, total_q,
+                              max_seqlen_q, total_k, H, H_kv, D, scale, causal, dtype, descale_k,
+                              descale_v, workspace, workspace_bytes, stream=None) -> int:
+    """fa_fwd_paged_kv4 with the descales behind device pointers (None: 1)."""
+    dt = FA_DTYPE[dtype] if isinstance(dtype, str) else int(dtype)
+    c = CAUSAL[causal] if isinstance(causal, str) else int(causal)
+    return int(load().fa_fwd_paged_kv4_devscale(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_q,
+                                                seqused_k, block_table, int(n_seqs), int(max_pages),
+                                                int(page_size), int(num_pages), int(total_q),
+                                                int(max_seqlen_q), int(total_k), int(H), int(H_kv),
+                                                int(D), float(scale), c, dt, descale_k, descale_v,
+                                                workspace, int(workspace_bytes), stream))
 
 
 def fa_last_device_error(stream=None) -> int:

@@ -949,7 +949,8 @@ fa_status_t run_var(const void* q, const void* k, const void* v, void* o, float*
                     int64_t max_seqlen_q, int64_t H, int64_t H_kv, int64_t D, float scale,
                     int causal, fa_dtype_t dtype, const float* descale_q, const float* descale_k,
                     const float* descale_v, cudaStream_t stream, int n_splits = 1,
-                    void* workspace = nullptr, size_t workspace_bytes = 0, float o_scale = 1.0f) {
+                    void* workspace = nullptr, size_t workspace_bytes = 0, float o_scale = 1.0f,
+                    const float* factor_s = nullptr, const float* factor_o = nullptr) {
   const bool paged = block_table != nullptr;
   // ---- host-side checks: nothing below touches the device until they pass
   if (!q || !k || !v || !o || !lse || !cu_q) return FA_ERR_INVALID_ARG;
@@ -1044,6 +1045,9 @@ fa_status_t run_var(const void* q, const void* k, const void* v, void* o, float*
   p.descale_q = descale_q;
   p.descale_k = descale_k;
   p.descale_v = descale_v;
+  p.factor_s = factor_s;
+  p.factor_o = factor_o;
+  if (factor_s) p.scale_log2 = std::fabs(scale);
   p.o = o;
   p.lse = lse;
   p.err = dev.err_word;
@@ -1110,15 +1114,18 @@ fa_status_t wait_control(uint32_t** err, uint64_t* limit_ns) {
 
 namespace fa {
 // fa_fwd_varlen (16-bit) with O multiplied by o_scale before its rounding, for
-// values whose descale is not in v (the 4-bit cache's unpacked rows).
+// values whose descale is not in v (the 4-bit cache's unpacked rows); scale_at
+// and o_scale_at, where not null, are device numbers that scale and o_scale are
+// multiplied by.
 fa_status_t fwd_varlen_scaled(const void* q, const void* k, const void* v, void* o, float* lse,
                               const int32_t* cu_q, const int32_t* cu_k, int64_t n_seqs,
                               int64_t total_q, int64_t total_k, int64_t max_seqlen_q, int64_t H,
                               int64_t H_kv, int64_t D, float scale, int causal, fa_dtype_t dtype,
-                              float o_scale, cudaStream_t stream) {
+                              float o_scale, const float* scale_at, const float* o_scale_at,
+                              cudaStream_t stream) {
   return run_var(q, k, v, o, lse, cu_q, cu_k, nullptr, nullptr, n_seqs, 0, 0, 0, total_q, total_k,
                  max_seqlen_q, H, H_kv, D, scale, causal, dtype, nullptr, nullptr, nullptr, stream,
-                 1, nullptr, 0, o_scale);
+                 1, nullptr, 0, o_scale, scale_at, o_scale_at);
 }
 }  // namespace fa
 

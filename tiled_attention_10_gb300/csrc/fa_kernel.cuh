@@ -56,6 +56,7 @@
 #include <atomic>
 #include <cstdint>
 
+#include "fa_kv4.cuh"
 #include "fa_ptx.cuh"
 #include "fa_tmem_io.cuh"
 
@@ -105,6 +106,8 @@ struct KernelParams {
   const int32_t* block_table;  // [n_seqs, max_pages] page of each key block (paged)
   int32_t n_seqs, max_pages, page_size;
   float o_scale;               // varlen / paged, 16-bit: a factor of O (V's descale), else 1
+  const float* factor_s;       // varlen, 16-bit: device factors of the scores (scale_log2 is then
+  const float* factor_o;       // without log2(e)) and of O, or null
   int32_t q_pack_log2;         // GQA packing: a query tile holds 2^q_pack_log2 heads of
                                // each of 128 >> q_pack_log2 tokens (row = token * 2^.. + head)
   int32_t causal_br;           // causal mask aligned bottom-right (key j visible to
@@ -1130,6 +1133,7 @@ __device__ void softmax_role(const KernelParams& p, const CUtensorMap* tmO, cons
     o_mul = dv;  // (P's factor 256 is in l too: O / l cancels it)
   } else if constexpr (kVar) {
     o_mul = p.o_scale;
+    if (kMode == kModeVarlen && p.factor_s) sl2 = sl2 * kv4::descale_from(p.factor_s) * 1.4426950408889634f;
   }
   // A masked score is -inf and must give p = 0: keep the base-2 scale
   // strictly positive (a zero scale or descale becomes 1e-30, which changes
@@ -1264,7 +1268,10 @@ __device__ void softmax_role(const KernelParams& p, const CUtensorMap* tmO, cons
       m_run = mm;
     }
     // (A varlen / paged row that saw no key has l = 0: O = 0.)
-    const float inv = (kVar && l == 0.0f) ? 0.0f : o_mul / l;
+    float mul = o_mul;     // (the device's factor of O is read here: kept, it would cost a register)
+    if constexpr (kMode == kModeVarlen && !C::kFp8)
+      if (p.factor_o) mul *= kv4::descale_from(p.factor_o);
+    const float inv = (kVar && l == 0.0f) ? 0.0f : mul / l;
     const float c0 = a0 * inv, c1 = a1 * inv;  // O = c0 O0 (+ c1 O1 when merging)
     const uint32_t tO1 = tO + 128;               // slot 1's O (read when merging)
     // This warp's 32 rows: tokens [box_row0, box_row0 + box_toks).

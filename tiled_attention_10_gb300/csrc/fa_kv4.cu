@@ -32,6 +32,7 @@
 
 namespace {
 
+using fa::kv4::Descales;
 constexpr int kThreads = 256;
 
 struct RowParams {
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const __grid_con
   const int which = blockIdx.y, group = threadIdx.x % G;
   const int h_step = R % p.cache.H_kv, t_step = R / p.cache.H_kv;
   int t = threadIdx.x / G / p.cache.H_kv, h = threadIdx.x / G % p.cache.H_kv;
-  const float g = p.cache.descale[which];
+  const float g = fa::kv4::descale_of(p.cache, which);
   const uint16_t* const src = static_cast<const uint16_t*>(p.in[which]) + first * p.token_stride[which] + group * 16;
   uint4 next[2];
   auto load = [&]() {
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_read_kernel(const __grid_cons
 bool off(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
 fa_status_t check_rows(const void* k, const void* v, const int64_t* slot_map, const uint8_t* kc,
-                       const uint8_t* ks, const uint8_t* vc, const uint8_t* vs, float dk, float dv,
+                       const uint8_t* ks, const uint8_t* vc, const uint8_t* vs, const Descales& d,
                        int64_t n_tokens, int64_t H_kv, int64_t D, int64_t page_size,
                        int64_t num_pages, fa_dtype_t dtype) {
   if (!kc || !ks || !vc || !vs) return FA_ERR_INVALID_ARG;
@@ -240,8 +241,8 @@ fa_status_t check_rows(const void* k, const void* v, const int64_t* slot_map, co
   if (n_tokens > 0 && (!k || !v || !slot_map)) return FA_ERR_INVALID_ARG;
   if (dtype != FA_DTYPE_F16 && dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_FP8E4M3)
     return FA_ERR_INVALID_ARG;
-  const float lo = std::ldexp(1.0f, -100), hi = std::ldexp(1.0f, 100);
-  if (!(dk >= lo && dk <= hi && dv >= lo && dv <= hi)) return FA_ERR_INVALID_ARG;
+  const fa_status_t st = check_descales(d);
+  if (st != FA_OK) return st;
   if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
   if (dtype == FA_DTYPE_FP8E4M3 || !fa::kv4::page_size_ok(page_size)) return FA_ERR_UNSUPPORTED;
   if (off(k, 16) || off(v, 16) || off(slot_map, 8) || off(kc, 16) || off(vc, 16) || off(ks, 16) || off(vs, 16))
@@ -252,12 +253,12 @@ fa_status_t check_rows(const void* k, const void* v, const int64_t* slot_map, co
 }
 
 RowParams params(const uint8_t* kc, const uint8_t* ks, const uint8_t* vc, const uint8_t* vs,
-                 float dk, float dv, const int64_t* slot_map, int64_t n_tokens, int64_t H_kv,
+                 const Descales& d, const int64_t* slot_map, int64_t n_tokens, int64_t H_kv,
                  int64_t D, int64_t page_size, int64_t num_pages) {
   RowParams p = {};
   p.cache.codes[0] = const_cast<uint8_t*>(kc); p.cache.codes[1] = const_cast<uint8_t*>(vc);
   p.cache.scales[0] = const_cast<uint8_t*>(ks); p.cache.scales[1] = const_cast<uint8_t*>(vs);
-  p.cache.descale[0] = dk; p.cache.descale[1] = dv;
+  for (int i = 0; i < 2; ++i) { p.cache.descale[i] = d.value[i]; p.cache.descale_at[i] = d.at[i]; }
   p.cache.num_pages = num_pages;
   p.cache.page_size = static_cast<int32_t>(page_size);
   p.cache.H_kv = static_cast<int32_t>(H_kv);
@@ -276,18 +277,13 @@ fa_status_t launch(K kernel, const RowParams& p, int64_t blocks, cudaStream_t st
   return cudaLaunchKernelEx(&c.cfg, kernel, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-}  // namespace
-
-extern "C" {
-
-fa_status_t fa_kv4_write(const void* k, const void* v, const int64_t* slot_map, uint8_t* k_codes,
-                         uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales, float descale_k,
-                         float descale_v, int64_t n_tokens, int64_t H_kv, int64_t D,
-                         int64_t page_size, int64_t num_pages, const fa_strides_t* strides,
-                         fa_dtype_t dtype, cudaStream_t stream) {
+fa_status_t write_rows(const void* k, const void* v, const int64_t* slot_map, uint8_t* k_codes,
+                  uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales, const Descales& d,
+                  int64_t n_tokens, int64_t H_kv, int64_t D, int64_t page_size, int64_t num_pages,
+                  const fa_strides_t* strides, fa_dtype_t dtype, cudaStream_t stream) {
   if (!strides) return FA_ERR_INVALID_ARG;
-  const fa_status_t st = check_rows(k, v, slot_map, k_codes, k_scales, v_codes, v_scales, descale_k,
-                                    descale_v, n_tokens, H_kv, D, page_size, num_pages, dtype);
+  const fa_status_t st = check_rows(k, v, slot_map, k_codes, k_scales, v_codes, v_scales, d, n_tokens,
+                                    H_kv, D, page_size, num_pages, dtype);
   if (st != FA_OK) return st;
   for (int i = 0; i < 2; ++i) {
     if (strides[i].seq < 1 || strides[i].head < 1) return FA_ERR_INVALID_ARG;
@@ -296,8 +292,8 @@ fa_status_t fa_kv4_write(const void* k, const void* v, const int64_t* slot_map, 
       return FA_ERR_UNSUPPORTED;
   }
   if (n_tokens == 0) return FA_OK;
-  RowParams p = params(k_codes, k_scales, v_codes, v_scales, descale_k, descale_v, slot_map,
-                       n_tokens, H_kv, D, page_size, num_pages);
+  RowParams p = params(k_codes, k_scales, v_codes, v_scales, d, slot_map, n_tokens, H_kv, D, page_size,
+                       num_pages);
   p.in[0] = k; p.in[1] = v;
   for (int i = 0; i < 2; ++i) { p.token_stride[i] = strides[i].seq; p.head_stride[i] = strides[i].head; }
   const int64_t blocks = (n_tokens + p.tile - 1) / p.tile;
@@ -308,17 +304,16 @@ fa_status_t fa_kv4_write(const void* k, const void* v, const int64_t* slot_map, 
                  : launch(fa_kv4_write_kernel<__nv_bfloat16, 128>, p, blocks, stream);
 }
 
-fa_status_t fa_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
-                        const uint8_t* v_scales, const int64_t* slot_map, void* k_out, void* v_out,
-                        float descale_k, float descale_v, int64_t n_tokens, int64_t H_kv, int64_t D,
-                        int64_t page_size, int64_t num_pages, fa_dtype_t dtype,
-                        cudaStream_t stream) {
-  const fa_status_t st = check_rows(k_out, v_out, slot_map, k_codes, k_scales, v_codes, v_scales,
-                                    descale_k, descale_v, n_tokens, H_kv, D, page_size, num_pages, dtype);
+fa_status_t read_rows(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                 const uint8_t* v_scales, const int64_t* slot_map, void* k_out, void* v_out,
+                 const Descales& d, int64_t n_tokens, int64_t H_kv, int64_t D, int64_t page_size,
+                 int64_t num_pages, fa_dtype_t dtype, cudaStream_t stream) {
+  const fa_status_t st = check_rows(k_out, v_out, slot_map, k_codes, k_scales, v_codes, v_scales, d,
+                                    n_tokens, H_kv, D, page_size, num_pages, dtype);
   if (st != FA_OK) return st;
   if (n_tokens == 0) return FA_OK;
-  RowParams p = params(k_codes, k_scales, v_codes, v_scales, descale_k, descale_v, slot_map,
-                       n_tokens, H_kv, D, page_size, num_pages);
+  RowParams p = params(k_codes, k_scales, v_codes, v_scales, d, slot_map, n_tokens, H_kv, D, page_size,
+                       num_pages);
   p.out[0] = k_out; p.out[1] = v_out;
   const int64_t blocks = (n_tokens + p.tile - 1) / p.tile;
   if (dtype == FA_DTYPE_F16)
@@ -326,6 +321,50 @@ fa_status_t fa_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales, const u
                    : launch(fa_kv4_read_kernel<__half, 128>, p, blocks, stream);
   return D == 64 ? launch(fa_kv4_read_kernel<__nv_bfloat16, 64>, p, blocks, stream)
                  : launch(fa_kv4_read_kernel<__nv_bfloat16, 128>, p, blocks, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status_t fa_kv4_write(const void* k, const void* v, const int64_t* slot_map, uint8_t* k_codes,
+                         uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales, float descale_k,
+                         float descale_v, int64_t n_tokens, int64_t H_kv, int64_t D,
+                         int64_t page_size, int64_t num_pages, const fa_strides_t* strides,
+                         fa_dtype_t dtype, cudaStream_t stream) {
+  return write_rows(k, v, slot_map, k_codes, k_scales, v_codes, v_scales, Descales{{descale_k, descale_v}, {}},
+               n_tokens, H_kv, D, page_size, num_pages, strides, dtype, stream);
+}
+
+fa_status_t fa_kv4_write_devscale(const void* k, const void* v, const int64_t* slot_map,
+                                  uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
+                                  uint8_t* v_scales, const float* descale_k, const float* descale_v,
+                                  int64_t n_tokens, int64_t H_kv, int64_t D, int64_t page_size,
+                                  int64_t num_pages, const fa_strides_t* strides, fa_dtype_t dtype,
+                                  cudaStream_t stream) {
+  return write_rows(k, v, slot_map, k_codes, k_scales, v_codes, v_scales,
+               Descales{{1.0f, 1.0f}, {descale_k, descale_v}}, n_tokens, H_kv, D, page_size, num_pages,
+               strides, dtype, stream);
+}
+
+fa_status_t fa_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                        const uint8_t* v_scales, const int64_t* slot_map, void* k_out, void* v_out,
+                        float descale_k, float descale_v, int64_t n_tokens, int64_t H_kv, int64_t D,
+                        int64_t page_size, int64_t num_pages, fa_dtype_t dtype,
+                        cudaStream_t stream) {
+  return read_rows(k_codes, k_scales, v_codes, v_scales, slot_map, k_out, v_out,
+              Descales{{descale_k, descale_v}, {}}, n_tokens, H_kv, D, page_size, num_pages, dtype, stream);
+}
+
+fa_status_t fa_kv4_read_devscale(const uint8_t* k_codes, const uint8_t* k_scales,
+                                 const uint8_t* v_codes, const uint8_t* v_scales,
+                                 const int64_t* slot_map, void* k_out, void* v_out,
+                                 const float* descale_k, const float* descale_v, int64_t n_tokens,
+                                 int64_t H_kv, int64_t D, int64_t page_size, int64_t num_pages,
+                                 fa_dtype_t dtype, cudaStream_t stream) {
+  return read_rows(k_codes, k_scales, v_codes, v_scales, slot_map, k_out, v_out,
+              Descales{{1.0f, 1.0f}, {descale_k, descale_v}}, n_tokens, H_kv, D, page_size, num_pages, dtype,
+              stream);
 }
 
 }  // extern "C"

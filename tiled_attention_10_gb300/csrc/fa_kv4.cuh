@@ -9,6 +9,8 @@
 
 #include <cstdint>
 
+#include "../../include/fa_api.h"
+
 namespace fa {
 namespace kv4 {
 
@@ -16,9 +18,20 @@ struct Cache {
   uint8_t* codes[2];    // K, V: [num_pages, H_kv, page_size, D / 2]
   uint8_t* scales[2];   // K, V: [num_pages, H_kv, page_size, D / 16]
   float descale[2];
+  const float* descale_at[2];   // where the descales are on the device, or null: the numbers above
   int64_t num_pages;
   int32_t page_size, H_kv;
 };
+
+// Descales are in [2^-100, 2^100]: a host's are refused outside, a device's moved
+// to the nearer end (NaN to the lower), so that no value becomes NaN by them.
+constexpr float kMinDescale = 0x1p-100f, kMaxDescale = 0x1p100f;
+__device__ __forceinline__ float descale_from(const float* at) {
+  return fminf(fmaxf(*at, kMinDescale), kMaxDescale);
+}
+__device__ __forceinline__ float descale_of(const Cache& c, int which) {   // (after wait_for_stream)
+  return c.descale_at[which] ? descale_from(c.descale_at[which]) : c.descale[which];
+}
 
 // Four bytes of codes (eight values) as four f16 pairs, low nibble first; and
 // two e4m3 scales as one f16 pair.  Both conversions are exact, and so is the
@@ -62,7 +75,7 @@ __device__ __forceinline__ void unpack_rows(const Cache& c, int which, const int
   const int piece = threadIdx.x % P;
   const int h_step = R % c.H_kv, t_step = R / c.H_kv;
   int t = threadIdx.x / P / c.H_kv, h = threadIdx.x / P % c.H_kv;
-  const float g = c.descale[which];
+  const float g = descale_of(c, which);
   uint4* dst = reinterpret_cast<uint4*>(out) + threadIdx.x;
   while (t < n) {
     uint32_t codes[kAhead], scale[kAhead];
@@ -100,6 +113,19 @@ __device__ __forceinline__ void unpack_rows(const Cache& c, int which, const int
     }
     dst += static_cast<int64_t>(kAhead) * THREADS;
   }
+}
+
+// An entry point's descales: numbers, or where they are on the device (null: the numbers).
+struct Descales {
+  float value[2];
+  const float* at[2];
+};
+inline fa_status_t check_descales(const Descales& d) {
+  for (int i = 0; i < 2; ++i) {
+    if (!(d.value[i] >= kMinDescale && d.value[i] <= kMaxDescale)) return FA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(d.at[i]) % 4 != 0) return FA_ERR_MISALIGNED;
+  }
+  return FA_OK;
 }
 
 // The paged attention's page sizes: tiles of 16 keys lie in one page.

@@ -51,12 +51,14 @@
 #include "fa_kv4_wide.cuh"
 
 namespace fa {
-// The packed forward with a factor on O (fa_api.cu).
+// The packed forward with a factor on O, and one each on the scores and on O
+// that are read on the device where the pointers are not null (fa_api.cu).
 fa_status_t fwd_varlen_scaled(const void* q, const void* k, const void* v, void* o, float* lse,
                               const int32_t* cu_q, const int32_t* cu_k, int64_t n_seqs,
                               int64_t total_q, int64_t total_k, int64_t max_seqlen_q, int64_t H,
                               int64_t H_kv, int64_t D, float scale, int causal, fa_dtype_t dtype,
-                              float o_scale, cudaStream_t stream);
+                              float o_scale, const float* scale_at, const float* o_scale_at,
+                              cudaStream_t stream);
 // The current device's error word for bounded waits, and their limit (fa_api.cu).
 fa_status_t wait_control(uint32_t** err, uint64_t* limit_ns);
 }  // namespace fa
@@ -216,6 +218,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, Cfg<D, NT>::kBlocks)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float w_max[kWarps][kRows], w_sum[kWarps][kRows], row_scale[kRows];
   __shared__ int row_limit[kRows];
+  __shared__ float factors[2];            // of the scores, of V
   __shared__ int64_t scan[kWarps];
   __shared__ Cursor cursor;
   __shared__ Unit units[4];               // of a ring: this one, the next two
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, Cfg<D, NT>::kBlocks)
   fa::wait_for_stream();
   fa::let_next_start();
 
-  if (!begin_units<kRows, kWarps * 32>(p, scan, cursor, units)) return;
+  if (!begin_units<kRows, kWarps * 32>(p, scan, cursor, units, factors)) return;
 
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * C::kWarpBytes;
   uint8_t* const ring_p = smem + warp * C::kWarpBytes;
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, Cfg<D, NT>::kBlocks)
       if (p.causal == FA_CAUSAL_TOP_LEFT) see = min(see, tok + 1);
       if (p.causal == FA_CAUSAL_BOTTOM_RIGHT) see = min(see, tok + 1 + u.keys - u.q_len);
       if (t == 0) {
-        row_scale[r] = fmaxf(p.sl2 * rescale, 1e-30f);
+        row_scale[r] = fmaxf(factors[0] * rescale, 1e-30f);
         row_limit[r] = see;
       }
     }
@@ -566,7 +569,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, Cfg<D, NT>::kBlocks)
       if (un.piece < 0) {
         const int row = un.row0 + r, tok = row / p.G, h = head * p.G + (row - tok * p.G);
         const int64_t to = (un.q_row0 + tok) * p.H + h;
-        const float dv = p.cache.descale[1] * inv;
+        const float dv = factors[1] * inv;
         T* dst = static_cast<T*>(p.o) + to * D + d;
         if (std::is_same<T, __half>::value)
           *reinterpret_cast<__half2*>(dst) = __floats2half2_rn(x * dv, y * dv);
@@ -792,15 +795,19 @@ fa_status_t fa_fwd_paged_kv4_workspace_size(int64_t n_seqs, int64_t max_seqlen_q
   return FA_OK;
 }
 
-fa_status_t fa_fwd_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_t* k_scales,
-                             const uint8_t* v_codes, const uint8_t* v_scales, void* o, float* lse,
-                             const int32_t* cu_seqlens_q, const int32_t* seqused_k,
-                             const int32_t* block_table, int64_t n_seqs, int64_t max_pages_per_seq,
-                             int64_t page_size, int64_t num_pages, int64_t total_q,
-                             int64_t max_seqlen_q, int64_t total_k, int64_t H, int64_t H_kv,
-                             int64_t D, float scale, int causal, fa_dtype_t dtype, float descale_k,
-                             float descale_v, void* workspace, size_t workspace_bytes,
-                             cudaStream_t stream) {
+}  // extern "C"
+
+namespace {
+
+fa_status_t attend(const void* q, const uint8_t* k_codes, const uint8_t* k_scales,
+                   const uint8_t* v_codes, const uint8_t* v_scales, void* o, float* lse,
+                   const int32_t* cu_seqlens_q, const int32_t* seqused_k,
+                   const int32_t* block_table, int64_t n_seqs, int64_t max_pages_per_seq,
+                   int64_t page_size, int64_t num_pages, int64_t total_q, int64_t max_seqlen_q,
+                   int64_t total_k, int64_t H, int64_t H_kv, int64_t D, float scale, int causal,
+                   fa_dtype_t dtype, const Descales& d, void* workspace, size_t workspace_bytes,
+                   cudaStream_t stream) {
+  const float descale_k = d.value[0], descale_v = d.value[1];
   if (!k_codes || !k_scales || !v_codes || !v_scales || !cu_seqlens_q || !seqused_k ||
       !block_table || !workspace || (total_q != 0 && (!q || !o || !lse)))
     return FA_ERR_INVALID_ARG;
@@ -810,8 +817,8 @@ fa_status_t fa_fwd_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_
   if (causal < 0 || causal > 2) return FA_ERR_INVALID_ARG;
   if (dtype != FA_DTYPE_F16 && dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_FP8E4M3)
     return FA_ERR_INVALID_ARG;
-  const float lo = std::ldexp(1.0f, -100), hi = std::ldexp(1.0f, 100);
-  if (!(descale_k >= lo && descale_k <= hi && descale_v >= lo && descale_v <= hi)) return FA_ERR_INVALID_ARG;
+  const fa_status_t ds = check_descales(d);
+  if (ds != FA_OK) return ds;
   if (!std::isfinite(scale) || !std::isfinite(scale * descale_k)) return FA_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
   if (dtype == FA_DTYPE_FP8E4M3 || !fa::kv4::page_size_ok(page_size)) return FA_ERR_UNSUPPORTED;
@@ -870,15 +877,15 @@ fa_status_t fa_fwd_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_
       e = D == 64 ? launch_unpack<__nv_bfloat16, 64>(u, sms, stream) : launch_unpack<__nv_bfloat16, 128>(u, sms, stream);
     if (e != cudaSuccess) return FA_ERR_CUDA;
     return fa::fwd_varlen_scaled(q, u.out[0], u.out[1], o, lse, cu_seqlens_q, u.cu_k, n_seqs, total_q, total_k,
-                                 max_seqlen_q, H, H_kv, D, scale * descale_k, causal, dtype, descale_v, stream);
+                                 max_seqlen_q, H, H_kv, D, scale * descale_k, causal, dtype, descale_v, d.at[0],
+                                 d.at[1], stream);
   }
 
   const int nt = tiles_for(rows);
   const Layout l = stream_layout(D, nt);
   AttnParams p = {};
   p.cache = c;
-  p.cache.descale[0] = descale_k;
-  p.cache.descale[1] = descale_v;
+  for (int i = 0; i < 2; ++i) { p.cache.descale[i] = d.value[i]; p.cache.descale_at[i] = d.at[i]; }
   p.q = q; p.o = o; p.lse = lse;
   p.cu_q = cu_seqlens_q; p.seqused_k = seqused_k; p.block_table = block_table;
   p.part_o = reinterpret_cast<float*>(ws + l.part_o);
@@ -886,7 +893,7 @@ fa_status_t fa_fwd_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_
   p.meta = reinterpret_cast<Meta*>(ws + l.meta);
   p.total_q = total_q;
   p.max_keys = max_pages_per_seq * page_size;
-  p.sl2 = std::fabs(scale) * descale_k * 1.4426950408889634f;
+  p.scale = std::fabs(scale);
   p.negate = scale < 0.0f ? 1 : 0;
   p.n_seqs = static_cast<int32_t>(n_seqs);
   p.max_pages = static_cast<int32_t>(max_pages_per_seq);
@@ -908,6 +915,41 @@ fa_status_t fa_fwd_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_
     e = D == 64 ? launch_stream_rows<__nv_bfloat16, 64>(p, nt, sms, stream)
                 : launch_stream_rows<__nv_bfloat16, 128>(p, nt, sms, stream);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status_t fa_fwd_paged_kv4(const void* q, const uint8_t* k_codes, const uint8_t* k_scales,
+                             const uint8_t* v_codes, const uint8_t* v_scales, void* o, float* lse,
+                             const int32_t* cu_seqlens_q, const int32_t* seqused_k,
+                             const int32_t* block_table, int64_t n_seqs, int64_t max_pages_per_seq,
+                             int64_t page_size, int64_t num_pages, int64_t total_q,
+                             int64_t max_seqlen_q, int64_t total_k, int64_t H, int64_t H_kv,
+                             int64_t D, float scale, int causal, fa_dtype_t dtype, float descale_k,
+                             float descale_v, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream) {
+  return attend(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_seqlens_q, seqused_k, block_table,
+                n_seqs, max_pages_per_seq, page_size, num_pages, total_q, max_seqlen_q, total_k, H, H_kv,
+                D, scale, causal, dtype, Descales{{descale_k, descale_v}, {}}, workspace, workspace_bytes,
+                stream);
+}
+
+fa_status_t fa_fwd_paged_kv4_devscale(const void* q, const uint8_t* k_codes, const uint8_t* k_scales,
+                                      const uint8_t* v_codes, const uint8_t* v_scales, void* o,
+                                      float* lse, const int32_t* cu_seqlens_q,
+                                      const int32_t* seqused_k, const int32_t* block_table,
+                                      int64_t n_seqs, int64_t max_pages_per_seq, int64_t page_size,
+                                      int64_t num_pages, int64_t total_q, int64_t max_seqlen_q,
+                                      int64_t total_k, int64_t H, int64_t H_kv, int64_t D,
+                                      float scale, int causal, fa_dtype_t dtype,
+                                      const float* descale_k, const float* descale_v,
+                                      void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return attend(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_seqlens_q, seqused_k, block_table,
+                n_seqs, max_pages_per_seq, page_size, num_pages, total_q, max_seqlen_q, total_k, H, H_kv,
+                D, scale, causal, dtype, Descales{{1.0f, 1.0f}, {descale_k, descale_v}}, workspace,
+                workspace_bytes, stream);
 }
 
 }  // extern "C"

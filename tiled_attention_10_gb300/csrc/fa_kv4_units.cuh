@@ -45,7 +45,7 @@ struct AttnParams {
   float* part_lse;        // [blocks, 2, rows]
   struct Meta* meta;      // [blocks]
   int64_t total_q, max_keys;
-  float sl2;              // |scale| * descale_k * log2(e)
+  float scale;            // |scale|
   int32_t n_seqs, max_pages, page_shift;   // page_shift: log2(page_size), or -1
   int32_t H, G, causal, negate;            // G = H / H_kv
 };
@@ -58,6 +58,11 @@ struct Meta {
   int32_t row0;      // first row (token * G + head) of the tile
   int32_t rows;      // rows of the tile that exist
 };
+
+// What turns a score of codes and scales into a power of two.
+__device__ __forceinline__ float score_scale(const AttnParams& p) {
+  return p.scale * descale_of(p.cache, 0) * 1.4426950408889634f;
+}
 
 struct Seq {
   int64_t q_row0;
@@ -159,13 +164,15 @@ static __device__ __noinline__ void next_unit(const AttnParams& p, Cursor& c, Un
 
 // The block's run of the work and the sequence it starts in, and its first two
 // units; false where there is no work for it.  For a block of THREADS; scan:
-// shared, THREADS / 32 entries.
+// shared, THREADS / 32 entries; factors: shared, score_scale and V's descale,
+// written here so that their loads overlap those of the lengths.
 template <int ROWS, int THREADS>
-__device__ __forceinline__ bool begin_units(const AttnParams& p, int64_t* scan, Cursor& cursor, Unit* units) {
+__device__ __forceinline__ bool begin_units(const AttnParams& p, int64_t* scan, Cursor& cursor, Unit* units, float* factors) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.n_seqs + THREADS - 1) / THREADS;
   const int s0 = min(p.n_seqs, tid * per), s1 = min(p.n_seqs, s0 + per);
   int64_t mine = 0;
+  const float factor[2] = {score_scale(p), descale_of(p.cache, 1)};
   Seq sq = {};
   for (int s = s0; s < s1; ++s) {
     sq = sequence<ROWS>(p, s);
@@ -178,6 +185,7 @@ __device__ __forceinline__ bool begin_units(const AttnParams& p, int64_t* scan, 
     if (lane >= o) incl += a;
   }
   if (lane == 31) scan[warp] = incl;
+  if (tid < 2) factors[tid] = factor[tid];
   __syncthreads();
   int64_t before = incl - mine, total = 0;
 #pragma unroll
@@ -230,6 +238,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_kv4_merge_kernel(const __
   fa::wait_for_stream();
   fa::let_next_start();
   const Meta mt = p.meta[blockIdx.x];
+  const float dv = descale_of(p.cache, 1);
   if (mt.pieces == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int share = 1;                         // warps a row
@@ -272,7 +281,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_kv4_merge_kernel(const __
     }
     if (in && part == 0) {
       const int row = mt.row0 + r, tok = row / p.G, h = mt.head0 + (row - tok * p.G);
-      const float mul = sum == 0.0f ? 0.0f : p.cache.descale[1] / sum;
+      const float mul = sum == 0.0f ? 0.0f : dv / sum;
       uint16_t* dst = static_cast<uint16_t*>(p.o) + ((mt.q_row0 + tok) * p.H + h) * D + lane * E;
 #pragma unroll
       for (int e = 0; e < E; e += 2) {

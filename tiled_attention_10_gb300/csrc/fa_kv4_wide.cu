@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
   __shared__ __align__(8) uint64_t barriers[kBarriers];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, drain_flag;
+  __shared__ float factors[2];            // of the scores, of V
   __shared__ int64_t scan[kThreads / 32];
   __shared__ Cursor cursor;
   __shared__ Unit units[4];
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
   fa::wait_for_stream();
   fa::let_next_start();
 
-  if (!begin_units<kRows, kThreads>(p, scan, cursor, units)) {
+  if (!begin_units<kRows, kThreads>(p, scan, cursor, units, factors)) {
     if (warp == kMmaWarp) fa::tmem_dealloc(tmem, 512);
     return;
   }
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
       asm volatile("bar.sync 1, 160;" ::: "memory");        // Q is there: the issuing warp joins
 
       // ---- softmax
-      const float sl2 = fmaxf(p.sl2 * rescale, 1e-30f);
+      const float sl2 = fmaxf(factors[0] * rescale, 1e-30f);
       int see = un.k_len;
       if (p.causal == FA_CAUSAL_TOP_LEFT) see = min(see, tok + 1);
       if (p.causal == FA_CAUSAL_BOTTOM_RIGHT) see = min(see, tok + 1 + un.keys - un.q_len);
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
         const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
         const float lse = l == 0.0f ? -CUDART_INF_F : (m - kBias + log2f(l)) * 0.69314718055994530942f;
         const bool whole = un.piece < 0;
-        const float mul = whole ? p.cache.descale[1] * inv : inv;
+        const float mul = whole ? factors[1] * inv : inv;
         const int h = head * p.G + (row - tok * p.G);
         const int64_t to = whole ? (un.q_row0 + tok) * p.H + h : (blockIdx.x * int64_t(2) + un.piece) * kRows + r;
 #pragma unroll 1

@@ -123,10 +123,12 @@ class KV4Cache:
 
     k_codes, v_codes: uint8 [num_pages, H_kv, page_size, D / 2]; k_scales,
     v_scales: float8_e4m3fn (or uint8) [num_pages, H_kv, page_size, D / 16].
-    k_descale, v_descale: floats.  A descale of largest value / (6 * 448) uses
-    the scales' whole range."""
+    k_descale, v_descale: floats, or tensors of one fp32 on the cache's device: those
+    are read by the kernels when they run (nothing synchronises, and a captured graph
+    follows them).  A descale of largest value / (6 * 448) uses the scales' whole
+    range."""
 
-    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "k_descale", "v_descale", "_geometry")
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "_descales", "_at", "_geometry")
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, k_descale=1.0, v_descale=1.0):
         if k_codes.dim() != 4:
@@ -139,8 +141,24 @@ class KV4Cache:
             kind = _U8 if t.dtype == _U8 else torch.float8_e4m3fn
             _check(name, t, kind, (pages, heads, rows, half // 8), index)
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
-        self.k_descale, self.v_descale = float(k_descale), float(v_descale)
         self._geometry = (pages, heads, rows, 2 * half, index)
+        self._set_descales(k_descale, v_descale)
+
+    def _set_descales(self, *descales):
+        got = []
+        for name, x in zip(("k_descale", "v_descale"), descales):
+            if isinstance(x, torch.Tensor):
+                if x.numel() != 1:
+                    raise ValueError(f"{name}: shape {tuple(x.shape)}, expected one number")
+                _check(name, x, torch.float32, x.shape, self._geometry[4])
+                got.append(x.detach())
+            else:
+                got.append(float(x))
+        self._descales, self._at = tuple(got), None
+        # If either is a tensor, both as tensors (a float goes to the device once) and their places.
+        if any(isinstance(x, torch.Tensor) for x in got):
+            at = [x if isinstance(x, torch.Tensor) else torch.full((1,), x, dtype=torch.float32, device=self.device) for x in got]
+            self._at = (at[0].data_ptr(), at[1].data_ptr(), at)
 
     @classmethod
     def allocate(cls, num_pages, page_size, H_kv, D, device="cuda", k_descale=1.0, v_descale=1.0):
@@ -149,6 +167,22 @@ class KV4Cache:
         codes = [torch.zeros(*shape, D // 2, dtype=torch.uint8, device=device) for _ in range(2)]
         scales = [torch.zeros(*shape, D // 16, dtype=torch.float8_e4m3fn, device=device) for _ in range(2)]
         return cls(codes[0], scales[0], codes[1], scales[1], k_descale, v_descale)
+
+    @property
+    def k_descale(self):
+        return self._descales[0]
+
+    @k_descale.setter
+    def k_descale(self, x):
+        self._set_descales(x, self._descales[1])
+
+    @property
+    def v_descale(self):
+        return self._descales[1]
+
+    @v_descale.setter
+    def v_descale(self, x):
+        self._set_descales(self._descales[0], x)
 
     @property
     def num_pages(self):
@@ -169,6 +203,14 @@ class KV4Cache:
     @property
     def device(self):
         return self.k_codes.device
+
+
+def _scaled(cache, host, device):
+    """(the entry point for the cache's descales, the two as its arguments)."""
+    at = cache._at
+    if at is None:
+        return host, *cache._descales
+    return device, at[0], at[1]
 
 
 def _rows(name, t, heads, d, index):
@@ -195,9 +237,11 @@ def kv4_write(k, v, slot_map, cache):
         raise ValueError("k and v must have the same type and shape")
     if not _is(slot_map, _I64, (n,), index):
         _check("slot_map", slot_map, _I64, (n,), index)
-    _call("fa_kv4_write", load().fa_kv4_write, index, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(),
+    lib = load()
+    fn, kd, vd = _scaled(cache, lib.fa_kv4_write, lib.fa_kv4_write_devscale)
+    _call("fa_kv4_write", fn, index, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(),
           cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr(),
-          cache.k_descale, cache.v_descale, n, heads, d, rows, pages, strides, dt)
+          kd, vd, n, heads, d, rows, pages, strides, dt)
 
 
 def kv4_read(cache, slot_map, dtype=torch.bfloat16, out=None):
@@ -216,9 +260,11 @@ def kv4_read(cache, slot_map, dtype=torch.bfloat16, out=None):
         for name, t in zip(("k", "v"), out):
             if not _is(t, dtype, (n, heads, d), index):
                 _check(name, t, dtype, (n, heads, d), index)
-    _call("fa_kv4_read", load().fa_kv4_read, index, cache.k_codes.data_ptr(), cache.k_scales.data_ptr(),
+    lib = load()
+    fn, kd, vd = _scaled(cache, lib.fa_kv4_read, lib.fa_kv4_read_devscale)
+    _call("fa_kv4_read", fn, index, cache.k_codes.data_ptr(), cache.k_scales.data_ptr(),
           cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), slot_map.data_ptr(), out[0].data_ptr(),
-          out[1].data_ptr(), cache.k_descale, cache.v_descale, n, heads, d, rows, pages, _dtype_of("out", out[0]))
+          out[1].data_ptr(), kd, vd, n, heads, d, rows, pages, _dtype_of("out", out[0]))
     return out
 
 
@@ -266,10 +312,12 @@ def paged_attention_kv4(q, cache, cu_seqlens_q, seqused_k, block_table, *, max_s
         workspace = paged_attention_kv4_workspace(q, cache, max_seqlen_q=max_seqlen_q, n_seqs=n, total_k=total_k)
     elif workspace.dim() != 1 or not _is(workspace, _U8, workspace.shape, index):
         _check("workspace", workspace, _U8, (None,), index)
-    _call("fa_fwd_paged_kv4", load().fa_fwd_paged_kv4, index, q.data_ptr(), cache.k_codes.data_ptr(),
+    lib = load()
+    fn, kd, vd = _scaled(cache, lib.fa_fwd_paged_kv4, lib.fa_fwd_paged_kv4_devscale)
+    _call("fa_fwd_paged_kv4", fn, index, q.data_ptr(), cache.k_codes.data_ptr(),
           cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), out.data_ptr(),
           lse.data_ptr(), cu_seqlens_q.data_ptr(), seqused_k.data_ptr(), block_table.data_ptr(), n, max_pages, rows,
           pages, total_q, max_seqlen_q, total_k, H, heads, d, 1.0 / math.sqrt(d) if scale is None else scale,
-          CAUSAL[causal] if isinstance(causal, str) else int(causal), dt, cache.k_descale, cache.v_descale,
+          CAUSAL[causal] if isinstance(causal, str) else int(causal), dt, kd, vd,
           workspace.data_ptr(), workspace.shape[0])
     return out, lse
