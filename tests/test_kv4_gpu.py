@@ -607,3 +607,35 @@ def test_descales_of_the_wrong_kind_are_refused(cuda_lib):
         c = fa.KV4Cache.allocate(1, 16, 1, 64)
         with pytest.raises((TypeError, ValueError)):
             c.v_descale = bad
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_read_rounds_once(cuda_lib, dtype):
+    """Every code and scale under descales that put products next to (not on) ties of the type,
+    where a rounding to fp32 in between takes them for the tie."""
+    dt, keep = DT[dtype], {"bf16": 16, "f16": 13}[dtype]
+    v = np.unique(np.outer(ref.E2M1, ref.e4m3_values()[:127]))
+    v = v[(v > 0.25) & (v < 64)]
+    g = np.random.default_rng(7).uniform(0.5, 1, 100000).astype(np.float32)
+    p = v.astype(np.float32)[None, :] * g[:, None]
+    near = ((p.view(np.uint32) & ((1 << keep) - 1)) == 1 << (keep - 1)) & (p.astype(np.float64) != v[None, :] * g[:, None].astype(np.float64))
+    chosen = g[near.any(1)][:12]
+    assert len(chosen) == 12
+    cache = fa.KV4Cache.allocate(16, 16, 1, 64)
+    # row r of page p: scale 8 p + r / 2 (no NaN), every code of both signs
+    codes = torch.arange(16, dtype=torch.uint8).repeat(4).view(32, 2)
+    cache.k_codes.copy_((codes[:, 0] | codes[:, 1] << 4).expand(16, 1, 16, 32))
+    cache.k_scales.view(torch.uint8).copy_((torch.arange(256) // 2).clamp(max=126).to(torch.uint8).view(16, 1, 16, 1).expand(16, 1, 16, 4))
+    cache.v_codes.copy_(cache.k_codes)
+    cache.v_scales.copy_(cache.k_scales)
+    slots = torch.arange(256, device="cuda")
+    for a in chosen:
+        cache.k_descale, cache.v_descale = float(a), float(a)
+        k, v = fa.kv4_read(cache, slots, dtype=dt)
+        assert torch.equal(k, v)
+        exact = ref.values(raw(cache.k_codes), raw(cache.k_scales), a).transpose(0, 2, 1, 3).reshape(256, 1, 64)
+        got = np64(k)
+        # no neighbour of the result is nearer (products of 30 bits, exact in 64)
+        for step in (torch.tensor(float("inf")), torch.tensor(float("-inf"))):
+            other = np64(torch.nextafter(k, step.to(dt).cuda().expand_as(k)))
+            assert (np.abs(got - exact) <= np.abs(other - exact)).all()

@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_read_kernel(const __grid_cons
   }
   __syncthreads();
   const int which = blockIdx.y;
-  fa::kv4::unpack_rows<T, D, kThreads>(p.cache, which, row, n,
+  fa::kv4::unpack_rows<T, D, kThreads, true>(p.cache, which, row, n,
                                        static_cast<uint16_t*>(p.out[which]) + first * p.cache.H_kv * D);
 }
 

@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/fa_api.h"
 
@@ -63,19 +64,48 @@ template <> __device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, f
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// a * b rounded to odd: the exact product where it is one, else the neighbour
+// whose last bit is set (the product cut short, with a bit for the rest), so that
+// rounding it to 16 bits gives the exact product's nearest: a second rounding to
+// nearest would take a product next to a tie for the tie.
+__device__ __forceinline__ float mul_to_odd(float a, float b) {
+  const float p = __fmul_rz(a, b);
+  return __uint_as_float(__float_as_uint(p) | (fmaf(a, b, -p) != 0.0f ? 1u : 0u));
+}
+
+// Whether any code * scale times g, in fp32, is a tie of the type T that the exact
+// product is not; only such a g needs mul_to_odd (of random ones 1 in 500 for f16;
+// 8192 tokens of 8 heads of 128 written and read: 21.9 us, 23.6 with it).  For a whole warp, a significand of code * scale
+// a lane: 8..15, and three times those.  An inexact product whose last set bit is
+// bit `low` is a tie of bf16 at 15, of f16 at 12, or at more where f16 is subnormal:
+// there the bit is 2^-25, the product below 2^(-1 - low), and reached if that is
+// not below g times the least code * scale, 2^-10.
+template <typename T>
+__device__ __forceinline__ bool rounds_twice(float g) {
+  const int lane = threadIdx.x & 31;
+  const float n = static_cast<float>((8 + (lane & 7)) * ((lane & 8) ? 3 : 1)), p = n * g;
+  const int low = __ffs(static_cast<int>(__float_as_uint(p) | 0x800000u)) - 1;
+  bool tie = low == 15;
+  if (std::is_same<T, __half>::value)
+    tie = low == 12 || (low > 12 && __uint_as_float(static_cast<uint32_t>(126 - low) << 23) >= g * 0x1p-10f);
+  return __any_sync(0xffffffffu, tie && fmaf(n, g, -p) != 0.0f);
+}
+
 // Rows of the cache as dense 16-bit rows out[r][head][D], r < n <= 32, by a block
 // of THREADS: row[r] is the index (page, head 0, row of the page) of token r in
 // the cache, negative for a row of zeros.  A thread unpacks 8 values at a time
 // (4 bytes of codes, one store of 16); consecutive threads take consecutive
-// pieces of the output, so the stores fill whole lines.
-template <typename T, int D, int THREADS>
+// pieces of the output, so the stores fill whole lines.  SCALED: times the descale
+// (else code * scale, which needs no rounding).
+template <typename T, int D, int THREADS, bool SCALED>
 __device__ __forceinline__ void unpack_rows(const Cache& c, int which, const int64_t* row, int n, void* out) {
   constexpr int P = D / 8, kAhead = 4;              // pieces of a head; pieces in flight
   constexpr int R = THREADS / P;                    // (token, head) rows the block takes at once
   const int piece = threadIdx.x % P;
   const int h_step = R % c.H_kv, t_step = R / c.H_kv;
   int t = threadIdx.x / P / c.H_kv, h = threadIdx.x / P % c.H_kv;
-  const float g = descale_of(c, which);
+  const float g = SCALED ? descale_of(c, which) : 1.0f;
+  const bool careful = SCALED && rounds_twice<T>(g);
   uint4* dst = reinterpret_cast<uint4*>(out) + threadIdx.x;
   while (t < n) {
     uint32_t codes[kAhead], scale[kAhead];
@@ -100,13 +130,20 @@ __device__ __forceinline__ void unpack_rows(const Cache& c, int which, const int
     for (int k = 0; k < kAhead; ++k) {
       if (k < last) {
         uint32_t v[4], w[4];
+        float2 f[4];
         codes_to_half(codes[k], v);
         const uint32_t s2 = scales_to_half(scale[k] * 0x101u);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t x = mul_half(v[j], s2);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
-          w[j] = pack16<T>(f.x * g, f.y * g);
+          f[j] = __half22float2(*reinterpret_cast<const __half2*>(&x));
+        }
+        if (careful) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = pack16<T>(mul_to_odd(f[j].x, g), mul_to_odd(f[j].y, g));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = pack16<T>(f[j].x * g, f[j].y * g);
         }
         dst[static_cast<int64_t>(k) * THREADS] = make_uint4(w[0], w[1], w[2], w[3]);
       }

@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kUnpackThreads) fa_kv4_unpack_kernel(const __g
   __syncthreads();
   for (int b = 0; base < rows; base += step, b ^= 1) {
     look(base + step, where[b ^ 1]);
-    fa::kv4::unpack_rows<T, D, kUnpackThreads>(p.cache, which, where[b],
+    fa::kv4::unpack_rows<T, D, kUnpackThreads, false>(p.cache, which, where[b],
                                                static_cast<int>(min(static_cast<int64_t>(kUnpackRows), rows - base)),
                                                static_cast<uint16_t*>(p.out[which]) + base * p.cache.H_kv * D);
     __syncthreads();
@@ -862,7 +862,6 @@ fa_status_t attend(const void* q, const uint8_t* k_codes, const uint8_t* k_scale
     u.cache = c;
     // Keys and values keep their exact values: K's descale goes into the softmax
     // scale, V's into the factor of O before its rounding.
-    u.cache.descale[0] = u.cache.descale[1] = 1.0f;
     u.cu_q = cu_seqlens_q; u.seqused_k = seqused_k; u.block_table = block_table;
     u.cu_k = reinterpret_cast<int32_t*>(ws);
     u.out[0] = ws + l.k; u.out[1] = ws + l.v;
