@@ -228,3 +228,24 @@ def test_captured_training_step(cuda_lib):
     got = [t.clone() for t in got]
     want = step([t.detach().clone().requires_grad_() for t in static])
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rot", [(64, 16), (64, 48), (128, 32), (128, 112)])
+def test_what_is_not_rotated_passes_unchanged(cuda_lib, D, rot, interleaved):
+    """Infinities, NaN and negative zeros among the elements behind the rotation, both ways (a
+    NaN's payload apart)."""
+    q, k, _, pos, freq, _, _ = make(1, 21, 3, 2, D, rot, 1, "BSND", "bf16", 11)
+    for x in (q, k):
+        rest = x[..., rot:]
+        rest[:, ::2, :, ::3] = float("inf")
+        rest[:, ::3, :, 1::4] = -float("inf")
+        rest[:, 1::4, :, 2::5] = float("nan")
+        rest[:, 1::2, :, ::2] = -0.0
+    kw = dict(norm=False, interleaved=interleaved, layout="BSND")
+    for got in (fa.qk_norm_rope(q, k, pos, freq, **kw), fa.qk_norm_rope_backward(q, k, q, k, pos, freq, **kw)[:2]):
+        for x, y in zip((q, k), got):
+            a, b = (t[..., rot:].contiguous() for t in (x, y))
+            assert torch.equal(a.isnan(), b.isnan())
+            assert torch.equal(a.view(torch.int16)[~a.isnan()], b.view(torch.int16)[~a.isnan()])
+            assert torch.isfinite(y[..., :rot]).all()

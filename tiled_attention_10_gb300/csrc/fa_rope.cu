@@ -202,7 +202,10 @@ __device__ __forceinline__ void warp_angles(const RopeParams& p, int64_t token, 
     if (lane + 32 * j < p.rot / 2) table[lane + 32 * j] = angle(p, token, lane + 32 * j);
 }
 
-// A lane's four pairs: cosines and sines (turned back with direction -1).
+// A lane's four pairs: cosines and sines (turned back with direction -1).  A lane
+// without pairs turns nothing: by a cosine of 1 and a sine of 0, an infinity would
+// make its neighbour NaN.  (PART: there may be such lanes.  Asked in every kernel,
+// that cost the full rotations 2 to 4 %.)
 struct Turn {
   F2 cs[2], sn[2], minus_sn[2];     // of pairs 0 1 and 2 3
 };
@@ -264,7 +267,7 @@ __device__ __forceinline__ void heads_of(const RopeParams& p, int part, int whic
 
 constexpr int kFwdRows = 2;   // rows a lane loads ahead
 
-template <typename T, int D, bool INTERLEAVED, bool NORM>
+template <typename T, int D, bool INTERLEAVED, bool NORM, bool PART>
 __global__ void __launch_bounds__(kFwdWarps * 32, 4) fa_rope_fwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LANES = D / 8, PER = 32 / LANES;   // lanes a head, heads a warp at once
   __shared__ float2 table[kFwdWarps][kMaxPairs];
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 4) fa_rope_fwd_kernel(const __
 #pragma unroll
           for (int j = 0; j < 4; ++j) y[j] = y[j] * rr * w[j];
         }
-        turn<INTERLEAVED>(y, t);
+        if (!PART || e.pair >= 0) turn<INTERLEAVED>(y, t);
         if (h < last) store_row<T>(dst + h * out_step, e, y);
       }
     }
@@ -424,7 +427,7 @@ struct Feed {
 
 constexpr int kStages = 7;
 
-template <typename T, int D, bool INTERLEAVED, bool NORM>
+template <typename T, int D, bool INTERLEAVED, bool NORM, bool PART>
 __global__ void __launch_bounds__(kBwdWarps * 32, kBwdResident) fa_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LANES = D / 8, PER = 32 / LANES;
   constexpr int kBytes = 2 * kStepBytes;
@@ -472,7 +475,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdResident) fa_rope_bwd_kern
         if (NORM) unpack<T>(load_row(reinterpret_cast<const uint16_t*>(st + kStepBytes) + slot * D, e), xv);
         ahead.step(p, stages + (stage == 0 ? kStages - 1 : stage - 1) * kBytes, lane);
         stage = stage == kStages - 1 ? 0 : stage + 1;
-        turn<INTERLEAVED>(g, t);
+        if (!PART || e.pair >= 0) turn<INTERLEAVED>(g, t);
         if (NORM) {
           F2 u[4];
 #pragma unroll
@@ -682,29 +685,37 @@ int64_t steps_of(int64_t H, int64_t H_kv, int64_t D) {
   return (H + per - 1) / per + (H_kv + per - 1) / per;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool PART>
 cudaError_t launch_fwd(const RopeParams& p, bool interleaved, bool norm, int64_t grid, cudaStream_t stream) {
   const fa::Launch c(dim3(static_cast<unsigned>(grid)), kFwdWarps * 32, 0, stream);
   if (interleaved)
-    return norm ? cudaLaunchKernelEx(&c.cfg, fa_rope_fwd_kernel<T, D, true, true>, p)
-                : cudaLaunchKernelEx(&c.cfg, fa_rope_fwd_kernel<T, D, true, false>, p);
-  return norm ? cudaLaunchKernelEx(&c.cfg, fa_rope_fwd_kernel<T, D, false, true>, p)
-              : cudaLaunchKernelEx(&c.cfg, fa_rope_fwd_kernel<T, D, false, false>, p);
+    return norm ? cudaLaunchKernelEx(&c.cfg, fa_rope_fwd_kernel<T, D, true, true, PART>, p)
+                : cudaLaunchKernelEx(&c.cfg, fa_rope_fwd_kernel<T, D, true, false, PART>, p);
+  return norm ? cudaLaunchKernelEx(&c.cfg, fa_rope_fwd_kernel<T, D, false, true, PART>, p)
+              : cudaLaunchKernelEx(&c.cfg, fa_rope_fwd_kernel<T, D, false, false, PART>, p);
+}
+template <typename T, int D>
+cudaError_t launch_fwd(const RopeParams& p, bool interleaved, bool norm, int64_t grid, cudaStream_t stream) {
+  return p.rot < D ? launch_fwd<T, D, true>(p, interleaved, norm, grid, stream)
+                   : launch_fwd<T, D, false>(p, interleaved, norm, grid, stream);
 }
 
+template <typename T, int D, bool PART>
+cudaError_t launch_bwd_rows(const RopeParams& p, bool interleaved, bool norm, int64_t grid, cudaStream_t stream) {
+  const fa::Launch c(dim3(static_cast<unsigned>(grid)), kBwdWarps * 32, 0, stream);
+  if (interleaved)
+    return norm ? cudaLaunchKernelEx(&c.cfg, fa_rope_bwd_kernel<T, D, true, true, PART>, p)
+                : cudaLaunchKernelEx(&c.cfg, fa_rope_bwd_kernel<T, D, true, false, PART>, p);
+  return norm ? cudaLaunchKernelEx(&c.cfg, fa_rope_bwd_kernel<T, D, false, true, PART>, p)
+              : cudaLaunchKernelEx(&c.cfg, fa_rope_bwd_kernel<T, D, false, false, PART>, p);
+}
 template <typename T, int D>
 cudaError_t launch_bwd(const RopeParams& p, bool interleaved, bool norm, int64_t grid, void* dwq,
                        void* dwk, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
-  if (grid > 0) {
-    const fa::Launch c(dim3(static_cast<unsigned>(grid)), kBwdWarps * 32, 0, stream);
-    if (interleaved)
-      e = norm ? cudaLaunchKernelEx(&c.cfg, fa_rope_bwd_kernel<T, D, true, true>, p)
-               : cudaLaunchKernelEx(&c.cfg, fa_rope_bwd_kernel<T, D, true, false>, p);
-    else
-      e = norm ? cudaLaunchKernelEx(&c.cfg, fa_rope_bwd_kernel<T, D, false, true>, p)
-               : cudaLaunchKernelEx(&c.cfg, fa_rope_bwd_kernel<T, D, false, false>, p);
-  }
+  if (grid > 0)
+    e = p.rot < D ? launch_bwd_rows<T, D, true>(p, interleaved, norm, grid, stream)
+                  : launch_bwd_rows<T, D, false>(p, interleaved, norm, grid, stream);
   if (e != cudaSuccess || !(dwq || dwk)) return e;
   const fa::Launch c(dim3(2 * D / 32), 1024, 0, stream);
   return cudaLaunchKernelEx(&c.cfg, fa_rope_dw_kernel<T>, static_cast<const float*>(p.partial),
