@@ -225,3 +225,27 @@ def test_bwd_workload_sampled_heads(name, cuda_lib):
             assert (err <= lim).all(), (nm, b, hk, float((err / lim).max()))
             print(f"{name} (b={b}, hk={hk}) {nm}: max|err|={err.max():.3g} "
                   f"max err/bound={(err / lim).max():.3f}")
+
+
+@pytest.mark.parametrize("D,causal", [(64, False), (128, True)])
+def test_a_tiny_scale_under_large_queries(cuda_lib, D, causal):
+    """Queries times 2^100 and the scale times 2^-100 are the same scores: O, dK and dV bit for bit,
+    dQ times 2^-100 as far as its type goes."""
+    from tiled_attention_10_gb300 import flash_attention
+    g = torch.Generator().manual_seed(D)
+    q, k, v, do = (torch.randn(1, 2, 300, D, generator=g).bfloat16().cuda() for _ in range(4))
+
+    def run(a, scale):
+        leaves = [t.clone().requires_grad_() for t in (a, k, v)]
+        o = flash_attention(*leaves, causal=causal, scale=scale)
+        return o.detach(), *torch.autograd.grad(o, leaves, do)
+
+    up = 2.0 ** 100
+    o, dq, dk, dv = run(q, D ** -0.5)
+    o2, dq2, dk2, dv2 = run(q * up, D ** -0.5 / up)
+    assert torch.isfinite(o).all() and torch.equal(o, o2)
+    assert torch.equal(dk, dk2) and torch.equal(dv, dv2)
+    # below 2^-26 the scaled dQ is among bf16's subnormal numbers, 2^-133 apart: off by half of
+    # that (2^-34 times 2^-100), and dQ by its own half step of less than 2^-35
+    near = (dq.double() - dq2.double() * up).abs()
+    assert (near[dq.abs() >= 2.0 ** -26] == 0).all() and (near <= 2.0 ** -34 + 2.0 ** -35).all()

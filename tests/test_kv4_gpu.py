@@ -639,3 +639,17 @@ def test_read_rounds_once(cuda_lib, dtype):
         for step in (torch.tensor(float("inf")), torch.tensor(float("-inf"))):
             other = np64(torch.nextafter(k, step.to(dt).cuda().expand_as(k)))
             assert (np.abs(got - exact) <= np.abs(other - exact)).all()
+
+
+@pytest.mark.parametrize("on_device", [False, True])
+@pytest.mark.parametrize("qn", [1, 12, 40, 100])
+def test_the_least_descale_under_large_queries(cuda_lib, qn, on_device):
+    """K's descale 2^-100, made up for by bf16 queries of 1e27: ordinary scores, whichever way they go."""
+    kd = 2.0 ** -100
+    st = Step([qn, 1], [700, 90], 4, 2, 128, 16, "bf16", seed=31, std=1e-27, kd=kd)
+    if on_device:
+        st.cache.k_descale = one(kd)
+    st.q.mul_(1e27)
+    o, lse = st.run()
+    st.cache.k_descale = kd
+    st.check(o, lse)

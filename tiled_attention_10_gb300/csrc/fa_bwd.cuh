@@ -564,7 +564,7 @@ __device__ void dq_softmax(const BwdParams& p, uint32_t tmem, int warp, int lane
   const uint32_t tDP = tmem + lane_off + C::kDP + 64 * half;
   const uint32_t tDS = tmem + lane_off + C::kDS + 32 * half;
   // A masked score is -inf and must give p = 0: keep the scale positive.
-  const float sl2 = fmaxf(p.scale_log2, 1e-30f);
+  const float sl2 = fmaxf(p.scale_log2, 1.17549435e-38f);
   uint32_t s_ph = 0, dp_ph = 0;
   const int grid = gridDim.x, bid = blockIdx.x;
   for (int w = 0;; ++w) {
@@ -996,7 +996,7 @@ __device__ void kv_softmax(const BwdParams& p, uint32_t tmem, uint32_t smem, int
   const uint32_t tDP = tmem + lane_off + C::kDP + 64 * half;
   const uint32_t tDV = tmem + lane_off + C::kDV;
   const uint32_t tDK = tmem + lane_off + C::kDK;
-  const float sl2 = fmaxf(p.scale_log2, 1e-30f);
+  const float sl2 = fmaxf(p.scale_log2, 1.17549435e-38f);
   uint32_t s_ph = 0, dp_ph = 0;
   Ring<C::kStages> ring;
   const int grid = gridDim.x, bid = blockIdx.x;

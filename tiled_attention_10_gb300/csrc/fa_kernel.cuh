@@ -1136,9 +1136,9 @@ __device__ void softmax_role(const KernelParams& p, const CUtensorMap* tmO, cons
     if (kMode == kModeVarlen && p.factor_s) sl2 = sl2 * kv4::descale_from(p.factor_s) * 1.4426950408889634f;
   }
   // A masked score is -inf and must give p = 0: keep the base-2 scale
-  // strictly positive (a zero scale or descale becomes 1e-30, which changes
-  // no unmasked exponent by more than ~1e-29 relative).
-  sl2 = fmaxf(sl2, 1e-30f);
+  // strictly positive (a zero scale or descale becomes the least normal number;
+  // a larger one would stand above scales that large queries make up for).
+  sl2 = fmaxf(sl2, 1.17549435e-38f);
 
   uint32_t s_phase = 0u, o_phase = 0u, solo_phase = 0u;
   uint32_t ring_pos = 0u;   // K/V ring positions consumed by earlier items
