@@ -1,4 +1,8 @@
 """fa_paged_slots against the loop reference: every output exact, untouched table entries intact."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -7,6 +11,7 @@ import tiled_attention_10_gb300 as fa
 from tests import paged_reference as ref
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _case(seed, n, ps, cols, past_hi, new_hi, total_q, n_free, odd=False):
@@ -76,3 +81,24 @@ def test_slots_graph_replays_with_new_lengths(cuda_lib):
     graph.replay()
     want = ref.slots(past2, new, free, table, ps, 64)
     assert np.array_equal(want[4], got.slot_map.cpu().numpy()) and np.array_equal(want[2], d["table"].cpu().numpy())
+
+
+def run_alone(code):
+    """Python code in a process of its own: no larger launch before it has asked for shared memory."""
+    p = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]
+
+
+@pytest.mark.parametrize("n", [6111, 6112, 6128, 6143, 6144])
+def test_slots_around_48_kb_of_sums(cuda_lib, n):
+    run_alone(f"""
+import numpy as np, torch, tiled_attention_10_gb300 as fa
+from tests import paged_reference as ref
+past, new = np.arange({n}, dtype=np.int32) % 40, np.arange({n}, dtype=np.int32) % 3
+table, free = np.full(({n}, 3), -1, np.int32), np.arange(2 * {n}, dtype=np.int32)
+want = ref.slots(past, new, free, table, 16, int(new.sum()))
+d = [torch.from_numpy(a.copy()).cuda() for a in (past, new, free, table)]
+got = fa.paged_slots(*d, page_size=16, total_q=int(new.sum()))
+for w, t in zip((*want[:5], want[5]), (got.cu_seqlens_q, got.seqused_k, d[3], got.positions, got.slot_map, got.pages_taken)):
+    assert np.array_equal(np.asarray(w).reshape(-1), t.cpu().numpy().reshape(-1))
+""")

@@ -26,6 +26,10 @@ struct Launch {
   Launch(const Launch&) = delete;
 };
 
+// Dynamic shared memory that a kernel gets without asking: 48 KB less what it
+// declares itself (1 KB is kept for that here).
+constexpr size_t kFreeSmem = 47 * 1024;
+
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The next kernel on the stream may be placed once all blocks have come here (so

@@ -206,7 +206,7 @@ extern "C" fa_status_t fa_paged_slots(const int32_t* past_k, const int32_t* new_
   p.max_pages = static_cast<int32_t>(max_pages_per_seq);
   p.page_size = page_size;
   const size_t smem = static_cast<size_t>(n_seqs + 1) * 8;
-  if (smem > 48 * 1024 &&
+  if (smem > fa::kFreeSmem &&
       cudaFuncSetAttribute(fa_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>((FA_SLOTS_MAX_SEQS + 1) * 8)) != cudaSuccess)
     return FA_ERR_CUDA;
