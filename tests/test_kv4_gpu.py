@@ -1,6 +1,9 @@
 """The 4-bit cache: kv4_write and kv4_read against the exact reference (codes and scales bit by
 bit), and attention over it against 64-bit attention within bounds from its arithmetic."""
 import itertools
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -11,6 +14,7 @@ from tests import paged_reference as ref
 from tests.gpu_helpers import CANARY16, CANARY32
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 DT = {"bf16": torch.bfloat16, "f16": torch.float16}
 
 
@@ -653,3 +657,42 @@ def test_the_least_descale_under_large_queries(cuda_lib, qn, on_device):
     o, lse = st.run()
     st.cache.k_descale = kd
     st.check(o, lse)
+
+
+@pytest.mark.parametrize("n", [12127, 12128, 12200, 12287, 12288, 16384])
+def test_unpacking_around_48_kb_of_sums(cuda_lib, n):
+    """In a process of its own: no larger launch before it has asked for shared memory.  All sequences
+    share a page; each has a few of its keys, and every 50th a query."""
+    code = f"""
+import numpy as np, torch, tiled_attention_10_gb300 as fa
+from tests import paged_reference as ref
+n, g = {n}, torch.Generator().manual_seed(1)
+cache = fa.KV4Cache.allocate(1, 16, 1, 64, k_descale=0.003, v_descale=0.002)
+rows = [torch.randn(16, 1, 64, generator=g).half().cuda() for _ in range(2)]
+slots = torch.arange(16, device="cuda")
+fa.kv4_write(*rows, slots, cache)
+raw = lambda t: t.view(torch.uint8).cpu().numpy()[0, 0]
+k = ref.values(raw(cache.k_codes), raw(cache.k_scales), 0.003)
+v = ref.values(raw(cache.v_codes), raw(cache.v_scales), 0.002)
+has = torch.arange(n) % 50 == 0
+cu = torch.cat((torch.zeros(1, dtype=torch.int32), has.int().cumsum(0).int())).cuda()
+used = (torch.arange(n, dtype=torch.int32) % 16 + 1).cuda()
+q = torch.randn(int(has.sum()), 1024, 64, generator=g).half().cuda()          # 1024 heads on one: unpacked
+o, lse = fa.paged_attention_kv4(q, cache, cu, used, torch.zeros(n, 1, dtype=torch.int32, device="cuda"), max_seqlen_q=1,
+                                total_k=n * 17)
+lens = used.cpu()[has].numpy()
+q64 = q.double().cpu().numpy()
+s, reach = q64 @ k.T / 8, np.abs(q64) @ np.abs(k).T / 8                  # [rows, heads, keys]
+seen = np.arange(16)[None, None, :] < lens[:, None, None]
+s = np.where(seen, s, -np.inf)
+top = s.max(-1, keepdims=True)
+p = np.exp(s - top)
+l = p.sum(-1, keepdims=True)
+O, PV, L = p / l @ v, p / l @ np.abs(v), (top + np.log(l))[..., 0].T
+A = np.where(seen, reach, 0).max(-1).T
+bo, bl = ref.attend_bounds(O, PV, A, 16, 64, torch.float16, 2.0 ** -11, 0.0)
+assert (np.abs(o.double().cpu().numpy() - O) <= bo).all()
+assert (np.abs(lse.double().cpu().numpy() - L) <= bl).all()
+"""
+    p = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]

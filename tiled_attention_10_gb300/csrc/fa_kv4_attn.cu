@@ -760,7 +760,7 @@ cudaError_t launch_stream_rows(const AttnParams& p, int nt, int sms, cudaStream_
 template <typename T, int D>
 cudaError_t launch_unpack(const UnpackParams& p, int sms, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(p.n_seqs + 1) * 4;
-  if (smem > 48 * 1024) {
+  if (smem > fa::kFreeSmem) {
     const cudaError_t e = cudaFuncSetAttribute(fa_kv4_unpack_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>((kMaxUnpackSeqs + 1) * 4));
     if (e != cudaSuccess) return e;
