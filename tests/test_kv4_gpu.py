@@ -12,6 +12,7 @@ import torch
 import tiled_attention_10_gb300 as fa
 from tests import paged_reference as ref
 from tests.gpu_helpers import CANARY16, CANARY32
+from tiled_attention_10_gb300 import binding
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -696,3 +697,31 @@ assert (np.abs(lse.double().cpu().numpy() - L) <= bl).all()
 """
     p = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert p.returncode == 0, p.stderr[-2000:]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_whose_waits_run_out(cuda_lib, D):
+    """Waits limited to less than the work takes: the kernel gives up, ends and says so, and the next
+    calls are right.  (Every wait has its limit, so that nothing hangs.)"""
+    steps = [Step([9] * 3, [9000, 300, 5000], 8, 2, D, 64, "bf16", seed=33), Step([32] * 40, [700] * 40, 8, 2, D, 64, "bf16", seed=34)]
+    want = [st.run() for st in steps]
+    assert binding.fa_last_device_error() == 0
+    seen = set()
+    try:
+        for limit in (1, 100, 1000, 3000, 10000, 30000):
+            binding.fa_set_wait_limit_ns(limit)
+            for st, w in zip(steps, want):
+                got = st.run()
+                status = binding.fa_last_device_error()
+                seen.add(status)
+                assert status in ((5,) if limit == 1 else (0, 5))
+                if status == 0:
+                    assert torch.equal(got[0].view(torch.int16), w[0].view(torch.int16)) and torch.equal(got[1], w[1])
+    finally:
+        binding.fa_set_wait_limit_ns(0)
+    assert 5 in seen
+    for st, w in zip(steps, want):
+        for _ in range(3):
+            got = st.run()
+            assert torch.equal(got[0].view(torch.int16), w[0].view(torch.int16)) and torch.equal(got[1], w[1])
+    assert binding.fa_last_device_error() == 0

@@ -82,10 +82,26 @@ __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y,
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // mbar_wait of a whole warp, with one answer: a warp that gives up does so as
-// one, before its next tcgen05 instruction.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const fa::WaitCtl& c) {
-  return __all_sync(0xffffffffu, fa::mbar_wait(bar, parity, c));
+// one, before its next tcgen05 instruction.  mbar_wait's try_wait may itself
+// sleep for longer than this kernel's longest wait, so limits below kPollBelow,
+// which a test of giving up sets, take an instantiation that polls (5 % slower).
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, const fa::WaitCtl& c) {
+  const uint64_t t0 = fa::global_timer_ns();
+  while (!fa::mbar_test_wait(bar, parity)) {
+    if (*c.abort) return false;
+    if (fa::global_timer_ns() - t0 > c.limit_ns) {
+      atomicOr(c.err, fa::kErrTimeout);
+      *c.abort = 1;
+      return false;
+    }
+  }
+  return true;
 }
+template <bool POLL>
+__device__ __forceinline__ bool warp_wait_by(uint32_t bar, uint32_t parity, const fa::WaitCtl& c) {
+  return __all_sync(0xffffffffu, POLL ? poll(bar, parity, c) : fa::mbar_wait(bar, parity, c));
+}
+constexpr uint64_t kPollBelow = 100000;
 
 // One key row's codes and scales.
 template <int D>
@@ -94,7 +110,7 @@ struct KeyRow {
   uint2 scales;
 };
 
-template <typename T, int D>
+template <typename T, int D, bool POLL>
 __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_constant__ AttnParams p, uint32_t* err, uint64_t limit_ns) {
   using C = WideCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -131,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
   fa::tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const fa::WaitCtl wc{limit_ns, err, &abort_flag};
+  auto warp_wait = [](uint32_t b, uint32_t parity, const fa::WaitCtl& c) { return warp_wait_by<POLL>(b, parity, c); };
   fa::wait_for_stream();
   fa::let_next_start();
 
@@ -168,14 +185,14 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
           q[4 * i] = v.x; q[4 * i + 1] = v.y; q[4 * i + 2] = v.z; q[4 * i + 3] = v.w;
         }
       }
-      float rescale = 1.0f;
+      float rescale = factors[0];
       if (!std::is_same<T, __half>::value) {
         uint32_t top = 0u;
 #pragma unroll
         for (int i = 0; i < D / 2; ++i) top = max(top, max(q[i] & 0x7fffu, (q[i] >> 16) & 0x7fffu));
         const int e = min(max(static_cast<int>(top >> 7), 30), 254);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 + 127 - e) << 23);
-        rescale = __uint_as_float(static_cast<uint32_t>(e - 8) << 23);
+        rescale *= __uint_as_float(static_cast<uint32_t>(e - 8) << 23);
 #pragma unroll
         for (int i = 0; i < D / 2; ++i)
           q[i] = pack_half(__uint_as_float(q[i] << 16) * up, __uint_as_float(q[i] & 0xffff0000u) * up);
@@ -187,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
       asm volatile("bar.sync 1, 160;" ::: "memory");        // Q is there: the issuing warp joins
 
       // ---- softmax
-      const float sl2 = fmaxf(factors[0] * rescale, 1e-30f);
+      const float sl2 = fmaxf(rescale, 1e-30f);
       int see = un.k_len;
       if (p.causal == FA_CAUSAL_TOP_LEFT) see = min(see, tok + 1);
       if (p.causal == FA_CAUSAL_BOTTOM_RIGHT) see = min(see, tok + 1 + un.keys - un.q_len);
@@ -459,31 +476,37 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
             fa::umma_commit_if(leader, bar(kODone + slot));
           }
         }
-        if (!ok) {                          // products on their way end before the memory is freed
-          fa::umma_commit_if(leader, bar(kDrain));
-          const fa::WaitCtl last{limit_ns > 1000000u ? limit_ns : 1000000u, err, &drain_flag};
-          warp_wait(bar(kDrain), 0, last);
-        }
       } else if (warp == kMmaWarp + 1 && lane == 0 && un.more && units[(turn + 1) & 3].more) {
         next_unit<kRows>(p, cursor, units[(turn + 2) & 3]);
       }
       done += n;                            // all phases follow the blocks before this unit
       if (!next(ok, un.more)) break;
     }
-    if (warp == kMmaWarp) fa::tmem_dealloc(tmem, 512);
+    if (warp == kMmaWarp) {
+      // Whichever role ended the block, products on their way, and their arrivals at
+      // its barriers, end before its memory is freed.
+      fa::umma_commit_if(leader, bar(kDrain));
+      warp_wait(bar(kDrain), 0, fa::WaitCtl{2000000000ull, err, &drain_flag});
+      fa::tmem_dealloc(tmem, 512);
+    }
   }
 }
 
-template <typename T, int D>
-cudaError_t launch(const AttnParams& p, int sms, uint32_t* err, uint64_t limit_ns, cudaStream_t stream) {
+template <typename T, int D, bool POLL>
+cudaError_t launch_by(const AttnParams& p, int sms, uint32_t* err, uint64_t limit_ns, cudaStream_t stream) {
   constexpr int smem = WideCfg<D>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(fa_kv4_wide_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(fa_kv4_wide_kernel<T, D, POLL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const fa::Launch c(dim3(sms), kThreads, smem, stream);
-  e = cudaLaunchKernelEx(&c.cfg, fa_kv4_wide_kernel<T, D>, p, err, limit_ns);
+  e = cudaLaunchKernelEx(&c.cfg, fa_kv4_wide_kernel<T, D, POLL>, p, err, limit_ns);
   if (e != cudaSuccess) return e;
   const fa::Launch mc(dim3(sms), kMergeWarps * 32, 0, stream);
   return cudaLaunchKernelEx(&mc.cfg, fa_kv4_merge_kernel<T, D, kRows>, p);
+}
+template <typename T, int D>
+cudaError_t launch(const AttnParams& p, int sms, uint32_t* err, uint64_t limit_ns, cudaStream_t stream) {
+  return limit_ns < kPollBelow ? launch_by<T, D, true>(p, sms, err, limit_ns, stream)
+                               : launch_by<T, D, false>(p, sms, err, limit_ns, stream);
 }
 
 }  // namespace
