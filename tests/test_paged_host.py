@@ -253,3 +253,23 @@ def test_attention_devscale_refusals(built_lib, over, code):
         a["q"], a["kc"], a["ks"], a["vc"], a["vs"], a["o"], a["lse"], a["cu"], a["used"], a["table"], a["n"], a["cols"],
         a["ps"], a["pages"], a["tq"], a["mq"], a["tk"], a["H"], a["H_kv"], a["D"], a["scale"], a["causal"], a["dtype"],
         a["dk"], a["dv"], a["ws"], a["nbytes"]) == code
+
+
+def test_forward_mode_derivatives_are_refused():
+    """A dual tensor's tangent would be dropped: refused before anything else, in every place."""
+    import torch.autograd.forward_ad as fad
+
+    import tiled_attention_10_gb300 as fa
+    x, w = torch.ones(1, 2, 3, 64, dtype=torch.bfloat16), torch.ones(64, dtype=torch.bfloat16)
+    f = torch.ones(8, dtype=torch.float64)
+    with fad.dual_level():
+        dual = lambda t: fad.make_dual(t, torch.ones_like(t))
+        with pytest.raises(ValueError):                # no tangent: refused as CPU tensors
+            fa.qk_norm_rope(x, x)
+        for q, k, kw in ((dual(x), x, {}), (x, dual(x), {}), (x, x, dict(q_weight=dual(w))), (x, x, dict(k_weight=dual(w))),
+                         (x, x, dict(inv_freq=dual(f))), (dual(x.clone().requires_grad_()), x, {})):
+            with pytest.raises(NotImplementedError):
+                fa.qk_norm_rope(q, k, **kw)
+        for args in ((dual(x), x, x, x), (x, dual(x), x, x), (x, x, dual(x), x), (x, x, x, dual(x))):
+            with pytest.raises(NotImplementedError):
+                fa.qk_norm_rope_backward(*args, None, None)

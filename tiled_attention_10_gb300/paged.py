@@ -18,6 +18,7 @@ import struct
 from typing import NamedTuple
 
 import torch
+from torch.autograd import forward_ad
 
 from .binding import CAUSAL, FA_DTYPE, FaError, fa_fwd_paged_kv4_workspace_size, load
 
@@ -63,6 +64,14 @@ def _check(name, t, dtype, shape, index):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _no_tangents(name, *tensors):
+    """Raises where a tensor carries a forward-mode derivative: the kernels would drop it."""
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise NotImplementedError(f"{name} has no forward-mode derivative")
 
 
 def _dtype_of(name, t):

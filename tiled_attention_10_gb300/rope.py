@@ -8,7 +8,7 @@ import struct
 import torch
 
 from .binding import FaError, fa_qk_norm_rope_bwd_workspace_size, load
-from .paged import _call, _check, _dtype_of, _I32, _is
+from .paged import _call, _check, _dtype_of, _I32, _is, _no_tangents
 
 _F64 = torch.float64
 
@@ -154,6 +154,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
     """dq, dk, dq_weight, dk_weight of qk_norm_rope from the gradients of its
     outputs and its inputs.  A weight's gradient is None where the forward had no
     such weight, or with weight_grads=False."""
+    _no_tangents("qk_norm_rope_backward", dq_out, dk_out, q, k, q_weight, k_weight, inv_freq)
     dt = _dtype_of("q", q)
     B, S, H, H_kv, D, bsnd = _sizes(q, k, layout)
     index = q.get_device()
@@ -210,7 +211,9 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, *, q_weight=None, k_weight
     each pair, a sequence of ints (default: the first).  Pairs are elements
     (i, i + rot / 2), or neighbours with `interleaved`.  norm=False leaves out
     the norm, inv_freq=None the rotation.  `out`: a pair to write into, which may
-    be (q, k) themselves; only where no gradient is asked for."""
+    be (q, k) themselves; only where no gradient is asked for.  Forward-mode
+    derivatives (torch.autograd.forward_ad) are refused."""
+    _no_tangents("qk_norm_rope", q, k, q_weight, k_weight, inv_freq)
     wants = torch.is_grad_enabled() and (q.requires_grad or k.requires_grad
                                          or (q_weight is not None and q_weight.requires_grad)
                                          or (k_weight is not None and k_weight.requires_grad))
