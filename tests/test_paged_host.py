@@ -273,3 +273,13 @@ def test_forward_mode_derivatives_are_refused():
         for args in ((dual(x), x, x, x), (x, dual(x), x, x), (x, x, dual(x), x), (x, x, x, dual(x))):
             with pytest.raises(NotImplementedError):
                 fa.qk_norm_rope_backward(*args, None, None)
+
+
+def test_a_gradient_of_the_frequencies_is_refused():
+    import tiled_attention_10_gb300 as fa
+    x = torch.ones(1, 2, 3, 64, dtype=torch.bfloat16)
+    f = torch.ones(8, dtype=torch.float64, requires_grad=True)
+    with pytest.raises(ValueError, match="inv_freq"):
+        fa.qk_norm_rope(x, x, torch.zeros(3, dtype=torch.int32), f)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        fa.qk_norm_rope(x, x, torch.zeros(3, dtype=torch.int32), f)

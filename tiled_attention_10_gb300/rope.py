@@ -211,9 +211,11 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, *, q_weight=None, k_weight
     each pair, a sequence of ints (default: the first).  Pairs are elements
     (i, i + rot / 2), or neighbours with `interleaved`.  norm=False leaves out
     the norm, inv_freq=None the rotation.  `out`: a pair to write into, which may
-    be (q, k) themselves; only where no gradient is asked for.  Forward-mode
-    derivatives (torch.autograd.forward_ad) are refused."""
+    be (q, k) themselves; only where no gradient is asked for.  Gradients of
+    inv_freq and forward-mode derivatives (torch.autograd.forward_ad) are refused."""
     _no_tangents("qk_norm_rope", q, k, q_weight, k_weight, inv_freq)
+    if inv_freq is not None and inv_freq.requires_grad and torch.is_grad_enabled():
+        raise ValueError("inv_freq has no gradient: detach it")
     wants = torch.is_grad_enabled() and (q.requires_grad or k.requires_grad
                                          or (q_weight is not None and q_weight.requires_grad)
                                          or (k_weight is not None and k_weight.requires_grad))
