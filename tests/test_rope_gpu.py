@@ -249,3 +249,36 @@ def test_what_is_not_rotated_passes_unchanged(cuda_lib, D, rot, interleaved):
             assert torch.equal(a.isnan(), b.isnan())
             assert torch.equal(a.view(torch.int16)[~a.isnan()], b.view(torch.int16)[~a.isnan()])
             assert torch.isfinite(y[..., :rot]).all()
+
+
+def test_writing_over_a_saved_tensor_is_noticed(cuda_lib):
+    """Outputs written into tensors that autograd has saved: their backward says so."""
+    q, k, w, pos, freq, axis, _ = make(1, 20, 4, 2, 64, 64, 1, "BSND", "bf16", 12)
+    one = lambda t: torch.ones_like(t).requires_grad_()
+    y, z = q * one(q), k * one(k)
+    fa.qk_norm_rope(q, k, pos, freq, layout="BSND", out=(q, k))
+    for t in (y, z):
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            t.sum().backward()
+
+    lens = torch.full((2,), 10, dtype=torch.int32, device="cuda")
+    table = torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2)
+    sl = fa.paged_slots(lens, lens, lens, table, page_size=16, total_q=20)
+    y, _ = fa.qk_norm_rope(q.clone().requires_grad_(), k, sl.positions, freq, layout="BSND")
+    fa.paged_slots(lens + 3, lens, lens, table, page_size=16, total_q=20, out=sl)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+    cache = fa.KV4Cache.allocate(4, 16, 2, 64)
+    slots = torch.arange(20, device="cuda")
+    got = fa.kv4_read(cache, slots)
+    y = [t * one(t) for t in got]
+    fa.kv4_read(cache, slots, out=got)
+    p = q[0].clone()
+    cu, used = torch.tensor([0, 10, 20], dtype=torch.int32, device="cuda"), lens
+    o, lse = fa.paged_attention_kv4(p, cache, cu, used, table, max_seqlen_q=10)
+    y += [o * one(o), lse * one(lse)]
+    fa.paged_attention_kv4(p, cache, cu, used, table, max_seqlen_q=10, out=o, lse=lse)
+    for t in y:
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            t.sum().backward()

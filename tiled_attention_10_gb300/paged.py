@@ -19,6 +19,7 @@ from typing import NamedTuple
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version   # the kernels write by address: autograd is told
 
 from .binding import CAUSAL, FA_DTYPE, FaError, fa_fwd_paged_kv4_workspace_size, load
 
@@ -107,6 +108,7 @@ def paged_slots(past_k, new_q, free_pages, block_table, *, page_size, total_q, o
         _check("free_pages", free_pages, _I32, (None,), dev)
     if block_table.dim() != 2 or not _is(block_table, _I32, (n, block_table.shape[1]), dev):
         _check("block_table", block_table, _I32, (n, None), dev)
+    given = out
     if out is None:
         i32 = {"dtype": _I32, "device": past_k.device}
         out = PagedSlots(torch.empty(n + 1, **i32), torch.empty(n, **i32), torch.empty(total_q, **i32),
@@ -123,6 +125,7 @@ def paged_slots(past_k, new_q, free_pages, block_table, *, page_size, total_q, o
     _call("fa_paged_slots", load().fa_paged_slots, dev, past_k.data_ptr(), new_q.data_ptr(), free_pages.data_ptr(),
           free_pages.shape[0], block_table.data_ptr(), n, block_table.shape[1], page_size, total_q, cu.data_ptr(),
           used.data_ptr(), pos.data_ptr(), slot.data_ptr(), taken.data_ptr())
+    increment_version((block_table,) if given is None else (block_table, *given))
     return out
 
 
@@ -261,6 +264,7 @@ def kv4_read(cache, slot_map, dtype=torch.bfloat16, out=None):
     n = slot_map.shape[0]
     if not _is(slot_map, _I64, (n,), index):
         _check("slot_map", slot_map, _I64, (n,), index)
+    given = out
     if out is None:
         out = (torch.empty((n, heads, d), dtype=dtype, device=slot_map.device),
                torch.empty((n, heads, d), dtype=dtype, device=slot_map.device))
@@ -274,6 +278,8 @@ def kv4_read(cache, slot_map, dtype=torch.bfloat16, out=None):
     _call("fa_kv4_read", fn, index, cache.k_codes.data_ptr(), cache.k_scales.data_ptr(),
           cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), slot_map.data_ptr(), out[0].data_ptr(),
           out[1].data_ptr(), kd, vd, n, heads, d, rows, pages, _dtype_of("out", out[0]))
+    if given is not None:
+        increment_version(given)
     return out
 
 
@@ -307,6 +313,7 @@ def paged_attention_kv4(q, cache, cu_seqlens_q, seqused_k, block_table, *, max_s
         _check("cu_seqlens_q", cu_seqlens_q, _I32, (n + 1,), index)
         _check("seqused_k", seqused_k, _I32, (n,), index)
         _check("block_table", block_table, _I32, (n, max_pages), index)
+    given = [t for t in (out, lse) if t is not None]
     if out is None:
         out = torch.empty_like(q)
     elif not _is(out, q.dtype, (total_q, H, d), index):
@@ -329,4 +336,6 @@ def paged_attention_kv4(q, cache, cu_seqlens_q, seqused_k, block_table, *, max_s
           pages, total_q, max_seqlen_q, total_k, H, heads, d, 1.0 / math.sqrt(d) if scale is None else scale,
           CAUSAL[causal] if isinstance(causal, str) else int(causal), dt, kd, vd,
           workspace.data_ptr(), workspace.shape[0])
+    if given:
+        increment_version(given)
     return out, lse

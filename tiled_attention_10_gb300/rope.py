@@ -8,7 +8,7 @@ import struct
 import torch
 
 from .binding import FaError, fa_qk_norm_rope_bwd_workspace_size, load
-from .paged import _call, _check, _dtype_of, _I32, _is, _no_tangents
+from .paged import _call, _check, _dtype_of, _I32, _is, _no_tangents, increment_version
 
 _F64 = torch.float64
 
@@ -122,6 +122,7 @@ def _forward(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, pair_axis
     wk = _weight("k_weight", k_weight, D, q.dtype, index)
     q, qp, *qs = _place(q, bsnd)
     k, kp, *ks = _place(k, bsnd)
+    given = out
     if out is None:
         qo, qop, *qos = _new(q, B, S, H, D, bsnd)
         ko, kop, *kos = _new(k, B, S, H_kv, D, bsnd)
@@ -137,6 +138,8 @@ def _forward(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, pair_axis
     _call("fa_qk_norm_rope", load().fa_qk_norm_rope, index, qp, kp, qop, kop, wq, wk, _ptr(pos), _ptr(inv_freq), B, S,
           H, H_kv, D, rot, axes, axis, 1 if interleaved else 0, 1 if norm else 0, eps,
           _four_strides(*qs, *ks, *qos, *kos), dt)
+    if given is not None:
+        increment_version(given)
     return out
 
 
