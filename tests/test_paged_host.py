@@ -283,3 +283,28 @@ def test_a_gradient_of_the_frequencies_is_refused():
         fa.qk_norm_rope(x, x, torch.zeros(3, dtype=torch.int32), f)
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
         fa.qk_norm_rope(x, x, torch.zeros(3, dtype=torch.int32), f)
+
+
+def test_gradients_through_the_cache_are_refused():
+    """kv4_write and paged_attention_kv4 have none: refused where one is asked for, nowhere else."""
+    import types
+
+    import torch.autograd.forward_ad as fad
+
+    import tiled_attention_10_gb300 as fa
+    cache = types.SimpleNamespace(_geometry=(1, 2, 16, 64, 0))
+    x = torch.ones(3, 2, 64, dtype=torch.bfloat16)
+    g = x.clone().requires_grad_()
+    i = torch.zeros(1, dtype=torch.int32)
+    calls = (lambda t: fa.kv4_write(t, x, None, cache), lambda t: fa.kv4_write(x, t, None, cache),
+             lambda t: fa.paged_attention_kv4(t, cache, i, i, i.view(1, 1), max_seqlen_q=1))
+    for call in calls:
+        with pytest.raises(ValueError, match="no gradient"):
+            call(g)
+        for ok in (x, g.detach()):
+            with pytest.raises(ValueError, match="cuda:0"):          # only: not on a GPU
+                call(ok)
+        with torch.no_grad(), pytest.raises(ValueError, match="cuda:0"):
+            call(g)
+        with fad.dual_level(), pytest.raises(NotImplementedError):
+            call(fad.make_dual(x, torch.ones_like(x)))

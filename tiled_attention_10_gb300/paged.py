@@ -75,6 +75,14 @@ def _no_tangents(name, *tensors):
                 raise NotImplementedError(f"{name} has no forward-mode derivative")
 
 
+def _no_gradients(name, *tensors):
+    """Raises where a gradient through one of the tensors is asked for."""
+    for t in tensors:
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} has no gradient: detach its inputs or call it under torch.no_grad()")
+    _no_tangents(name, *tensors)
+
+
 def _dtype_of(name, t):
     code = _DTYPE.get(t.dtype)
     if code is None:
@@ -240,7 +248,9 @@ def _rows(name, t, heads, d, index):
 def kv4_write(k, v, slot_map, cache):
     """Writes rows k, v [n_tokens, H_kv, D] (fp16 / bf16, any token and head
     strides of 16-byte multiples) into the cache's slots slot_map (int64
-    [n_tokens]; -1 skips a row, the others must differ)."""
+    [n_tokens]; -1 skips a row, the others must differ).  No gradient goes
+    through the cache: rows that require one are refused (as by torch's out=)."""
+    _no_gradients("kv4_write", k, v)
     dt = _dtype_of("k", k)
     pages, heads, rows, d, index = cache._geometry
     n = k.shape[0]
@@ -302,7 +312,8 @@ def paged_attention_kv4(q, cache, cu_seqlens_q, seqused_k, block_table, *, max_s
     sequences' keys together; it sizes the workspace of long queries (default:
     what the block table can hold).  lse is [H, total_q].  `workspace` (see
     paged_attention_kv4_workspace) saves the allocation; calls that may overlap
-    need one each."""
+    need one each.  There is no gradient: queries that require one are refused."""
+    _no_gradients("paged_attention_kv4", q)
     dt = _dtype_of("q", q)
     pages, heads, rows, d, index = cache._geometry
     total_q, H, _ = q.shape
