@@ -308,3 +308,17 @@ def test_gradients_through_the_cache_are_refused():
             call(g)
         with fad.dual_level(), pytest.raises(NotImplementedError):
             call(fad.make_dual(x, torch.ones_like(x)))
+
+
+def test_causal_true_is_refused():
+    """It would have meant top-left: a decoding query over the first key alone."""
+    import types
+
+    import tiled_attention_10_gb300 as fa
+    cache = types.SimpleNamespace(_geometry=(1, 2, 16, 64, 0))
+    x, i = torch.ones(3, 2, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="bottom_right"):
+        fa.paged_attention_kv4(x, cache, i, i, i.view(1, 1), max_seqlen_q=1, causal=True)
+    for c in (False, 0, 1, 2, "none", "top_left"):
+        with pytest.raises(ValueError, match="cuda:0"):
+            fa.paged_attention_kv4(x, cache, i, i, i.view(1, 1), max_seqlen_q=1, causal=c)

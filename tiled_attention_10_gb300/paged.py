@@ -312,8 +312,11 @@ def paged_attention_kv4(q, cache, cu_seqlens_q, seqused_k, block_table, *, max_s
     sequences' keys together; it sizes the workspace of long queries (default:
     what the block table can hold).  lse is [H, total_q].  `workspace` (see
     paged_attention_kv4_workspace) saves the allocation; calls that may overlap
-    need one each.  There is no gradient: queries that require one are refused."""
+    need one each.  causal: "none", "top_left" or "bottom_right", as in the
+    varlen calls (True says neither and is refused).  There is no gradient: queries that require one are refused."""
     _no_gradients("paged_attention_kv4", q)
+    if causal is True:
+        raise ValueError('causal=True: say "bottom_right" (the default) or "top_left"')
     dt = _dtype_of("q", q)
     pages, heads, rows, d, index = cache._geometry
     total_q, H, _ = q.shape
