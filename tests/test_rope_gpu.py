@@ -282,3 +282,17 @@ def test_writing_over_a_saved_tensor_is_noticed(cuda_lib):
     for t in y:
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             t.sum().backward()
+
+
+def test_a_million_heads(cuda_lib):
+    """The most heads a call takes, of one token: what they are as heads of many tokens at its position."""
+    n, g = 1 << 20, torch.Generator(device="cuda").manual_seed(13)
+    x = [torch.randn(1, 1, n, 128, generator=g, device="cuda").bfloat16() for _ in range(4)]
+    freq = (10000.0 ** (-torch.arange(0, 128, 2, dtype=torch.float64) / 128)).cuda()
+    pos = torch.tensor([77], dtype=torch.int32, device="cuda")
+    many = [t.view(1, 2048, n // 2048, 128) for t in x]
+    for a, b in ((fa.qk_norm_rope(*x[:2], pos, freq, layout="BSND"), fa.qk_norm_rope(*many[:2], pos.expand(2048), freq, layout="BSND")),
+                 (fa.qk_norm_rope_backward(*x, pos, freq, layout="BSND")[:2],
+                  fa.qk_norm_rope_backward(*many, pos.expand(2048), freq, layout="BSND")[:2])):
+        for y, z in zip(a, b):
+            assert torch.isfinite(y).all() and torch.equal(y.view(-1), z.reshape(-1))

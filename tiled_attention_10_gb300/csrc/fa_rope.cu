@@ -675,10 +675,11 @@ int fwd_share(int64_t tokens) {
 }
 
 // Backward: parts a token's steps are cut into, so that there are tasks for all
-// warps of the grid: as few as that takes, two steps each at least.
+// warps of the grid: as few as that takes, two steps each at least (and steps *
+// parts a 32-bit number: a million heads a token are allowed).
 int bwd_share(int64_t tokens, int64_t steps) {
   const int64_t want = (int64_t(kBwdBlocks) * kBwdWarps + tokens - 1) / tokens;
-  return static_cast<int>(std::max<int64_t>(1, std::min(want, (steps + 1) / 2)));
+  return static_cast<int>(std::max<int64_t>(1, std::min({want, (steps + 1) / 2, INT32_MAX / steps})));
 }
 int64_t steps_of(int64_t H, int64_t H_kv, int64_t D) {
   const int64_t per = 256 / D;
