@@ -296,3 +296,12 @@ def test_a_million_heads(cuda_lib):
                   fa.qk_norm_rope_backward(*many, pos.expand(2048), freq, layout="BSND")[:2])):
         for y, z in zip(a, b):
             assert torch.isfinite(y).all() and torch.equal(y.view(-1), z.reshape(-1))
+
+
+def test_frequencies_from_2_to_the_64_on_read_as_zero(cuda_lib):
+    q, k, _, pos, _, _, _ = make(1, 20, 2, 1, 64, 16, 1, "BSND", "f16", 14, pos_lo=1)
+    big = torch.tensor([2.0 ** 64, -2.0 ** 64, 1.7 * 2.0 ** 64, 2.0 ** 65, 1e300, -1e300, float("inf"), 2.0 ** 64 * (1 + 2.0 ** -52)],
+                       dtype=torch.float64, device="cuda")
+    assert all(torch.equal(a, b) for a, b in zip(fa.qk_norm_rope(q, k, pos, big, norm=False, layout="BSND"), (q, k)))
+    below = torch.nextafter(big[0], big[0] * 0).expand(8).contiguous()
+    assert not torch.equal(fa.qk_norm_rope(q, k, pos, below, norm=False, layout="BSND")[0], q)

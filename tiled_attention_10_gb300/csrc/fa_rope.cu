@@ -172,7 +172,7 @@ __device__ __forceinline__ uint64_t turns_of(double f) {
   const uint64_t hi = __umul64hi(m, K);
   uint64_t fixed = 0ull;               // zero and tiny; 2^64 and more, infinite and NaN
   if (e <= 1 && e > -63) fixed = hi >> (1 - e);
-  if (e > 1 && e <= 64) fixed = (hi << (e - 1)) | ((m * K) >> (65 - e));
+  if (e > 1 && e < 64) fixed = (hi << (e - 1)) | ((m * K) >> (65 - e));
   return (bits >> 63) ? 0ull - fixed : fixed;
 }
 
