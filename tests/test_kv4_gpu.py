@@ -725,3 +725,33 @@ def test_many_rows_whose_waits_run_out(cuda_lib, D):
             got = st.run()
             assert torch.equal(got[0].view(torch.int16), w[0].view(torch.int16)) and torch.equal(got[1], w[1])
     assert binding.fa_last_device_error() == 0
+
+
+# ---------------------------------------------------------------- the way's own rounding of P
+def is_unpacked(st, max_q):
+    """Whether a call goes through unpacked rows (P in the queries' type) by the library's rule;
+    otherwise P is held in f16."""
+    rows = max_q * (st.H // st.H_kv)
+    return rows > (512 if sum(st.seq_k) // 2048 >= len(st.seq_k) else 128)
+
+
+@pytest.mark.parametrize("scale", [-0.08, 0.0, 1.0, 3.0])
+@pytest.mark.parametrize("qn,keys", [(40, (900, 333)), (64, (900, 333)), (65, (900, 333)), (200, (4000, 3000))])
+def test_scales_by_the_ways_bound(cuda_lib, scale, qn, keys):
+    st = Step([qn, qn - 3], list(keys), 4, 2, 128, 16, "bf16", seed=41)
+    st.check(*st.run(scale=scale), scale=scale, unpacked=is_unpacked(st, qn))
+
+
+@pytest.mark.parametrize("qn", [12, 40, 64, 65, 100])
+def test_bad_pages_by_the_ways_bound(cuda_lib, qn):
+    st = Step([qn, qn], [100, 70], 4, 2, 128, 16, "bf16", seed=42, bad_page=True)
+    st.check(*st.run(), unpacked=is_unpacked(st, qn))
+
+
+@pytest.mark.parametrize("std,mul", [(30.0, 1.0), (1.0, 1e-30), (1.0, 1e30), (1e-3, 1.0)])
+@pytest.mark.parametrize("qn", [20, 32, 33])
+def test_magnitudes_by_the_ways_bound(cuda_lib, std, mul, qn):
+    st = Step([qn, 12, 2], [700, 64, 90], 4, 1, 128, 32, "bf16", seed=43, std=std, kd=0.003 * std)
+    st.q.mul_(mul)
+    scale = 128 ** -0.5 / mul
+    st.check(*st.run(scale=scale), scale=scale, unpacked=is_unpacked(st, qn))
