@@ -604,7 +604,7 @@ struct UnpackParams {
   const int32_t* block_table;
   int32_t* cu_k;            // [n_seqs + 1], written
   void* out[2];             // [total_k, H_kv, D]
-  int64_t total_q, total_k, max_keys;
+  int64_t total_k, max_keys;
   int32_t n_seqs, max_pages;
 };
 
@@ -865,7 +865,7 @@ fa_status_t attend(const void* q, const uint8_t* k_codes, const uint8_t* k_scale
     u.cu_q = cu_seqlens_q; u.seqused_k = seqused_k; u.block_table = block_table;
     u.cu_k = reinterpret_cast<int32_t*>(ws);
     u.out[0] = ws + l.k; u.out[1] = ws + l.v;
-    u.total_q = total_q; u.total_k = total_k;
+    u.total_k = total_k;
     u.max_keys = max_pages_per_seq * page_size;
     u.n_seqs = static_cast<int32_t>(n_seqs);
     u.max_pages = static_cast<int32_t>(max_pages_per_seq);

@@ -378,10 +378,10 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// The copies' side of a walk: steps of x (forward), or of dy and, where X, x
-// into ring stages.  Addresses move on by a head stride; they are worked out
-// where a run of one kind of heads begins.
-template <int D, bool GRAD, bool X>
+// The copies' side of a walk: steps of dy and, where X, x into ring stages.
+// Addresses move on by a head stride; they are worked out where a run of one kind
+// of heads begins.
+template <int D, bool X>
 struct Feed {
   static constexpr int LANES = D / 8, PER = 32 / LANES;
   Walk<PER> w;
@@ -400,19 +400,17 @@ struct Feed {
     w.at += left;
     const int64_t e = (lane % LANES) * 8;
     if (X) x = static_cast<const uint16_t*>(p.x[k]) + row_base(p.st_x[k], w.b, w.s) + h * p.st_x[k].head + e;
-    if (GRAD) dy = static_cast<const uint16_t*>(p.dy[k]) + row_base(p.st_dy[k], w.b, w.s) + h * p.st_dy[k].head + e;
+    dy = static_cast<const uint16_t*>(p.dy[k]) + row_base(p.st_dy[k], w.b, w.s) + h * p.st_dy[k].head + e;
   }
   // One step (nothing once the work is all under way), as a group of its own.
   __device__ __forceinline__ void step(const RopeParams& p, uint32_t stage, int lane) {
     if (left > 0) {
       const int k = w.at > w.nq;
       const int bytes = h < h_end ? 16 : 0;
-      if (GRAD) {
-        copy16(stage + lane * 16, bytes ? dy : static_cast<const uint16_t*>(p.dy[0]), bytes);
-        dy += p.st_dy[k].head * PER;
-      }
+      copy16(stage + lane * 16, bytes ? dy : static_cast<const uint16_t*>(p.dy[0]), bytes);
+      dy += p.st_dy[k].head * PER;
       if (X) {
-        copy16(stage + (GRAD ? kStepBytes : 0) + lane * 16, bytes ? x : static_cast<const uint16_t*>(p.x[0]), bytes);
+        copy16(stage + kStepBytes + lane * 16, bytes ? x : static_cast<const uint16_t*>(p.x[0]), bytes);
         x += p.st_x[k].head * PER;
       }
       h += PER;
@@ -440,7 +438,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdResident) fa_rope_bwd_kern
   fa::let_next_start();
   const Elements e = elements<INTERLEAVED>(p.rot, sub);
   const uint32_t stages = static_cast<uint32_t>(__cvta_generic_to_shared(ring[warp]));
-  Feed<D, true, NORM> ahead(p, lane);
+  Feed<D, NORM> ahead(p, lane);
   Walk<PER> now(p);
 #pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) ahead.step(p, stages + i * kBytes, lane);
