@@ -755,3 +755,36 @@ def test_magnitudes_by_the_ways_bound(cuda_lib, std, mul, qn):
     st.q.mul_(mul)
     scale = 128 ** -0.5 / mul
     st.check(*st.run(scale=scale), scale=scale, unpacked=is_unpacked(st, qn))
+
+
+# One page, every table entry that page, and as many keys as a call takes: attention over it is
+# attention over the page alone, lse apart by log of the number of times.
+@pytest.mark.parametrize("qn,ps,rest", [(1, 128, 0), (1, 128, 31), (2, 128, 0), (2, 128, 100), (5, 128, 0), (5, 6016, 0), (1, 6016, 0)])
+def test_sequences_up_to_two_billion_keys(cuda_lib, qn, ps, rest):
+    most = (1 << 31) - 256
+    cols = most // ps
+    assert cols * ps == most                        # both page sizes divide it
+    g = torch.Generator().manual_seed(qn + ps)
+    cache = fa.KV4Cache.allocate(1, ps, 1, 64, k_descale=0.003, v_descale=0.002)
+    rows = [torch.randn(ps, 1, 64, generator=g).bfloat16().cuda() for _ in range(2)]
+    fa.kv4_write(*rows, torch.arange(ps, device="cuda"), cache)
+    q = torch.randn(qn, 8, 64, generator=g).bfloat16().cuda()
+    cu = torch.tensor([0, qn], dtype=torch.int32, device="cuda")
+    table = torch.zeros(1, cols, dtype=torch.int32, device="cuda")
+    n = most - rest
+    o, lse = fa.paged_attention_kv4(q, cache, cu, torch.tensor([n], dtype=torch.int32, device="cuda"), table, max_seqlen_q=qn,
+                                    causal="none")
+    assert binding.fa_last_device_error() == 0
+    k, v = (ref.gather(raw(a), raw(b), d, [0], ps, 1) for a, b, d in ((cache.k_codes, cache.k_scales, 0.003),
+                                                                      (cache.v_codes, cache.v_scales, 0.002)))
+    O, L, PV, A = ref.attend(np64(q), k, v, 64 ** -0.5, 0)
+    # The cut page changes O by no more than its share of the keys.  Sums over so many keys lose 2^-24
+    # an add, the matrix unit's perhaps twice that (its rounding is not documented): up to 16 rows 1824
+    # warps take 32 keys a step, 4 adds to a lane's sum and 2 products; above, 152 blocks take 128 keys,
+    # one add and 8 products.
+    steps = n / 32 / 1824 if qn * 8 <= 16 else n / 128 / 152
+    sums, products = (4 * steps, 2 * steps) if qn * 8 <= 16 else (steps, 8 * steps)
+    bo, bl = ref.attend_bounds(O, PV, A, ps, 64, torch.bfloat16, 2.0 ** -12, 0.0)
+    loss, share = sums * 2.0 ** -24, 2.0 * ps / n
+    assert (np.abs(np64(o) - O) <= bo + (loss + products * 2.0 ** -23 + share) * (PV + np.abs(O))).all()
+    assert (np.abs(np64(lse) - (L + np.log(n / ps))) <= bl + loss + share + 2.0 ** -24 * 22).all()

@@ -115,15 +115,16 @@ __device__ __forceinline__ int v_place(int r, int c) {
 }
 
 // Where the next step's keys are: pages of its two halves (one lookup when
-// pages hold 32 keys or more) and the first key's row in its page.
+// pages hold 32 keys or more) and the first key's row in its page.  A step ahead
+// of a sequence's last key may be past 2^31 (unsigned here).
 struct Place {
   int page[2], in_page;
 };
-__device__ __forceinline__ Place look_up(const AttnParams& p, uint32_t table, int key0, int end) {
+__device__ __forceinline__ Place look_up(const AttnParams& p, uint32_t table, uint32_t key0, uint32_t end) {
   Place at = {{-1, -1}, 0};
   if (key0 < end) {
-    const int ps = p.cache.page_size;
-    const int col = p.page_shift >= 0 ? key0 >> p.page_shift : key0 / ps;
+    const uint32_t ps = p.cache.page_size;
+    const uint32_t col = p.page_shift >= 0 ? key0 >> p.page_shift : key0 / ps;
     at.in_page = key0 - col * ps;
     at.page[0] = p.block_table[table + col];
     at.page[1] = ps >= kStep ? at.page[0] : key0 + 16 < end ? p.block_table[table + col + 1] : -1;
@@ -250,9 +251,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, Cfg<D, NT>::kBlocks)
   Place at;                                 // of the next step to load
   uint32_t table;                           // the sequence's row of the block table
   auto start_ring = [&](const Unit& u) {
-    const int end = u.key_end;
+    const uint32_t end = u.key_end;
     table = static_cast<uint32_t>(u.s) * static_cast<uint32_t>(p.max_pages);
-    int next = u.key_begin + warp * kStep;
+    uint32_t next = u.key_begin + warp * kStep;
     at = look_up(p, table, next, end);
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) {
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kWarps * 32, Cfg<D, NT>::kBlocks)
         const int next = key0 + (C::kStages - 1) * step;
         if (next < key_end) load_step<D>(p, me, ring + into * St::kBytes, head, next, key_end, at, lane);
         copies_commit();
-        at = look_up(p, table, next + step, key_end);
+        at = look_up(p, table, static_cast<uint32_t>(next) + step, key_end);
       }
 
       // S^T: two tiles of 16 keys

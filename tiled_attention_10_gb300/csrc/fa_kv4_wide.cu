@@ -355,12 +355,13 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
     const uint32_t tiles = smem + (which ? C::kV : C::kK);
     const int ps = p.cache.page_size;
     int key_begin, key_end, head;           // of the unit being loaded
-    uint32_t n, table;
+    uint32_t n, table, last;
     // A step's page is looked up before it is known whether the step is there
     // (of the unit's last key then): no branch, so nothing waits for the page.
-    auto key_of = [&](uint32_t j) { return key_begin + static_cast<int>(j) * kBlockKeys + r; };
+    // (Blocks ahead of the last key may be past 2^31: compared as unsigned numbers.)
+    auto key_of = [&](uint32_t j) { return static_cast<int>(static_cast<uint32_t>(key_begin) + j * kBlockKeys + r); };
     auto page_of = [&](uint32_t j) {
-      const int key = max(min(key_of(j), key_end - 1), 0);
+      const int key = static_cast<int>(min(static_cast<uint32_t>(key_of(j)), last));
       return __ldg(p.block_table + (table + (p.page_shift >= 0 ? key >> p.page_shift : key / ps)));
     };
     auto fetch = [&](uint32_t j, int page, KeyRow<D>& k) {
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) k.codes[i] = make_uint4(0u, 0u, 0u, 0u);
       k.scales = make_uint2(0u, 0u);
-      if (key < key_end && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.cache.num_pages)) {
+      if (static_cast<uint32_t>(key) < static_cast<uint32_t>(key_end) && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.cache.num_pages)) {
         const uint4* c = reinterpret_cast<const uint4*>(p.cache.codes[which] + static_cast<uint64_t>(at) * (D / 2));
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) k.codes[i] = __ldg(c + i);
@@ -402,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
     auto begin = [&](const Unit& un) {
       key_begin = un.key_begin;
       key_end = un.key_end;
+      last = max(key_end, 1) - 1;
       head = un.head;
       n = static_cast<uint32_t>((key_end - key_begin + kBlockKeys - 1) / kBlockKeys);
       table = static_cast<uint32_t>(un.s) * static_cast<uint32_t>(p.max_pages);
