@@ -788,3 +788,19 @@ def test_sequences_up_to_two_billion_keys(cuda_lib, qn, ps, rest):
     loss, share = sums * 2.0 ** -24, 2.0 * ps / n
     assert (np.abs(np64(o) - O) <= bo + (loss + products * 2.0 ** -23 + share) * (PV + np.abs(O))).all()
     assert (np.abs(np64(lse) - (L + np.log(n / ps))) <= bl + loss + share + 2.0 ** -24 * 22).all()
+
+
+def test_no_descales_are_ones(cuda_lib):
+    """Null device descales: 1."""
+    a, b = junk_cache(2, 16, 1, 64, 1.0, 1.0), junk_cache(2, 16, 1, 64, 1.0, 1.0)
+    x = torch.randn(20, 1, 64, generator=torch.Generator().manual_seed(6)).half().cuda() * 100
+    slots, stream = torch.arange(20, device="cuda"), torch.cuda.current_stream().cuda_stream
+    fa.kv4_write(x, x, slots, a)
+    ptrs = [t.data_ptr() for t in (b.k_codes, b.k_scales, b.v_codes, b.v_scales)]
+    assert binding.fa_kv4_write_devscale(x.data_ptr(), x.data_ptr(), slots.data_ptr(), *ptrs, None, None, 20, 1, 64, 16, 2,
+                                         [(64, 64, 64)] * 2, "f16", stream) == 0
+    assert all(torch.equal(s, t) for s, t in zip(cache_bits(a), cache_bits(b)))
+    k, v = torch.empty_like(x), torch.empty_like(x)
+    assert binding.fa_kv4_read_devscale(*ptrs, slots.data_ptr(), k.data_ptr(), v.data_ptr(), None, None, 20, 1, 64, 16, 2, "f16",
+                                        stream) == 0
+    assert all(torch.equal(s, t) for s, t in zip(fa.kv4_read(a, slots, torch.float16), (k, v)))

@@ -322,3 +322,17 @@ def test_causal_true_is_refused():
     for c in (False, 0, 1, 2, "none", "top_left"):
         with pytest.raises(ValueError, match="cuda:0"):
             fa.paged_attention_kv4(x, cache, i, i, i.view(1, 1), max_seqlen_q=1, causal=c)
+
+
+def test_a_gradient_of_a_descale_is_refused():
+    import tiled_attention_10_gb300 as fa
+    cache = object.__new__(fa.KV4Cache)
+    cache._geometry, cache._descales = (2, 1, 16, 64, 0), (1.0, 1.0)
+    for bad in (torch.ones(1, requires_grad=True), torch.ones((), requires_grad=True)):
+        with pytest.raises(ValueError, match="no gradient"):
+            cache.k_descale = bad
+        with pytest.raises(ValueError, match="no gradient"):
+            cache.v_descale = bad
+    with pytest.raises(ValueError, match="cuda:0"):                      # only: not on a GPU
+        cache.k_descale = torch.ones(1)
+    assert cache.k_descale == 1.0

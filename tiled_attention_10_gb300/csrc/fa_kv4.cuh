@@ -75,11 +75,12 @@ __device__ __forceinline__ float mul_to_odd(float a, float b) {
 
 // Whether any code * scale times g, in fp32, is a tie of the type T that the exact
 // product is not; only such a g needs mul_to_odd (of random ones 1 in 500 for f16;
-// 8192 tokens of 8 heads of 128 written and read: 21.9 us, 23.6 with it).  For a whole warp, a significand of code * scale
-// a lane: 8..15, and three times those.  An inexact product whose last set bit is
-// bit `low` is a tie of bf16 at 15, of f16 at 12, or at more where f16 is subnormal:
-// there the bit is 2^-25, the product below 2^(-1 - low), and reached if that is
-// not below g times the least code * scale, 2^-10.
+// 8192 tokens of 8 heads of 128 written and read: 21.9 us, 23.6 with it).  For a
+// whole warp, a significand of code * scale a lane: 8..15, and three times those.
+// An inexact product whose last set bit is bit `low` is a tie of bf16 at 15, of f16
+// at 12, or at more where f16 is subnormal: there the bit is 2^-25, the product
+// below 2^(-1 - low), and reached if that is not below g times the least
+// code * scale, 2^-10.
 template <typename T>
 __device__ __forceinline__ bool rounds_twice(float g) {
   const int lane = threadIdx.x & 31;

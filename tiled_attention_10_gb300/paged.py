@@ -76,10 +76,10 @@ def _no_tangents(name, *tensors):
 
 
 def _no_gradients(name, *tensors):
-    """Raises where a gradient through one of the tensors is asked for."""
+    """Raises where a gradient of one of the tensors is asked for: there is none."""
     for t in tensors:
         if t.requires_grad and torch.is_grad_enabled():
-            raise ValueError(f"{name} has no gradient: detach its inputs or call it under torch.no_grad()")
+            raise ValueError(f"{name} has no gradient: detach what goes in, or use torch.no_grad()")
     _no_tangents(name, *tensors)
 
 
@@ -170,6 +170,7 @@ class KV4Cache:
             if isinstance(x, torch.Tensor):
                 if x.numel() != 1:
                     raise ValueError(f"{name}: shape {tuple(x.shape)}, expected one number")
+                _no_gradients(name, x)
                 _check(name, x, torch.float32, x.shape, self._geometry[4])
                 got.append(x.detach())
             else:
@@ -313,7 +314,8 @@ def paged_attention_kv4(q, cache, cu_seqlens_q, seqused_k, block_table, *, max_s
     what the block table can hold).  lse is [H, total_q].  `workspace` (see
     paged_attention_kv4_workspace) saves the allocation; calls that may overlap
     need one each.  causal: "none", "top_left" or "bottom_right", as in the
-    varlen calls (True says neither and is refused).  There is no gradient: queries that require one are refused."""
+    varlen calls (True says neither and is refused).  There is no gradient:
+    queries that require one are refused."""
     _no_gradients("paged_attention_kv4", q)
     if causal is True:
         raise ValueError('causal=True: say "bottom_right" (the default) or "top_left"')
