@@ -743,7 +743,7 @@ UnpackLayout unpack_layout(int64_t n_seqs, int64_t total_k, int64_t H_kv, int64_
 template <typename T, int D, int NT>
 cudaError_t launch_stream(const AttnParams& p, int sms, cudaStream_t stream) {
   using C = Cfg<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(fa_kv4_attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  cudaError_t e = fa::allow_smem<fa_kv4_attn_kernel<T, D, NT>>(C::kSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(sms * C::kBlocks));
   const fa::Launch c(grid, C::kWarps * 32, C::kSmem, stream);

@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kv4_wide_kernel(const __grid_c
 template <typename T, int D, bool POLL>
 cudaError_t launch_by(const AttnParams& p, int sms, uint32_t* err, uint64_t limit_ns, cudaStream_t stream) {
   constexpr int smem = WideCfg<D>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(fa_kv4_wide_kernel<T, D, POLL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = fa::allow_smem<fa_kv4_wide_kernel<T, D, POLL>>(smem);
   if (e != cudaSuccess) return e;
   const fa::Launch c(dim3(sms), kThreads, smem, stream);
   e = cudaLaunchKernelEx(&c.cfg, fa_kv4_wide_kernel<T, D, POLL>, p, err, limit_ns);

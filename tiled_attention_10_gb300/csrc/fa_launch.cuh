@@ -6,9 +6,29 @@
  * and then lets the next kernel's blocks be placed too, as its own end.
  */
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 namespace fa {
+
+// The calling thread's current context (fa_api.cu).
+CUcontext current_context(int* dev_out);
+
+// Raises a kernel's limit of dynamic shared memory: once per device and context,
+// not at every call.
+template <auto KERNEL>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<CUcontext> known[64];
+  int dev = 0;
+  const CUcontext ctx = current_context(&dev);
+  const bool kept = ctx && dev >= 0 && dev < 64;
+  if (kept && known[dev].load(std::memory_order_acquire) == ctx) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && kept) known[dev].store(ctx, std::memory_order_release);
+  return e;
+}
 
 struct Launch {
   cudaLaunchConfig_t cfg = {};

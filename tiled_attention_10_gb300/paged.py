@@ -19,12 +19,12 @@ from typing import NamedTuple
 
 import torch
 from torch.autograd import forward_ad
-from torch.autograd.graph import increment_version   # the kernels write by address: autograd is told
 
 from .binding import CAUSAL, FA_DTYPE, FaError, fa_fwd_paged_kv4_workspace_size, load
 
 _I32, _I64, _U8 = torch.int32, torch.int64, torch.uint8
 _DTYPE = {torch.float16: FA_DTYPE["f16"], torch.bfloat16: FA_DTYPE["bf16"]}
+_written = torch._C._increment_version      # (tensors): the kernels write by address, autograd is told
 _two_strides = struct.Struct("6q").pack     # two fa_strides_t
 
 
@@ -69,10 +69,9 @@ def _check(name, t, dtype, shape, index):
 
 def _no_tangents(name, *tensors):
     """Raises where a tensor carries a forward-mode derivative: the kernels would drop it."""
-    if forward_ad._current_level >= 0:
-        for t in tensors:
-            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
-                raise NotImplementedError(f"{name} has no forward-mode derivative")
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"{name} has no forward-mode derivative")
 
 
 def _no_gradients(name, *tensors):
@@ -133,7 +132,7 @@ def paged_slots(past_k, new_q, free_pages, block_table, *, page_size, total_q, o
     _call("fa_paged_slots", load().fa_paged_slots, dev, past_k.data_ptr(), new_q.data_ptr(), free_pages.data_ptr(),
           free_pages.shape[0], block_table.data_ptr(), n, block_table.shape[1], page_size, total_q, cu.data_ptr(),
           used.data_ptr(), pos.data_ptr(), slot.data_ptr(), taken.data_ptr())
-    increment_version((block_table,) if given is None else (block_table, *given))
+    _written((block_table,) if given is None else (block_table, *given))
     return out
 
 
@@ -148,7 +147,7 @@ class KV4Cache:
     follows them).  A descale of largest value / (6 * 448) uses the scales' whole
     range."""
 
-    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "_descales", "_at", "_geometry")
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "_descales", "_at", "_held", "_geometry")
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, k_descale=1.0, v_descale=1.0):
         if k_codes.dim() != 4:
@@ -179,7 +178,7 @@ class KV4Cache:
         # If either is a tensor, both as tensors (a float goes to the device once) and their places.
         if any(isinstance(x, torch.Tensor) for x in got):
             at = [x if isinstance(x, torch.Tensor) else torch.full((1,), x, dtype=torch.float32, device=self.device) for x in got]
-            self._at = (at[0].data_ptr(), at[1].data_ptr(), at)
+            self._at, self._held = (at[0].data_ptr(), at[1].data_ptr()), at
 
     @classmethod
     def allocate(cls, num_pages, page_size, H_kv, D, device="cuda", k_descale=1.0, v_descale=1.0):
@@ -226,14 +225,6 @@ class KV4Cache:
         return self.k_codes.device
 
 
-def _scaled(cache, host, device):
-    """(the entry point for the cache's descales, the two as its arguments)."""
-    at = cache._at
-    if at is None:
-        return host, *cache._descales
-    return device, at[0], at[1]
-
-
 def _rows(name, t, heads, d, index):
     """The (batch, head, seq) strides of rows t [n, H_kv, D] with D contiguous."""
     if t.dim() != 3 or t.shape[1:] != (heads, d):
@@ -251,7 +242,8 @@ def kv4_write(k, v, slot_map, cache):
     strides of 16-byte multiples) into the cache's slots slot_map (int64
     [n_tokens]; -1 skips a row, the others must differ).  No gradient goes
     through the cache: rows that require one are refused (as by torch's out=)."""
-    _no_gradients("kv4_write", k, v)
+    if k.requires_grad or v.requires_grad or forward_ad._current_level >= 0:
+        _no_gradients("kv4_write", k, v)
     dt = _dtype_of("k", k)
     pages, heads, rows, d, index = cache._geometry
     n = k.shape[0]
@@ -260,8 +252,8 @@ def kv4_write(k, v, slot_map, cache):
         raise ValueError("k and v must have the same type and shape")
     if not _is(slot_map, _I64, (n,), index):
         _check("slot_map", slot_map, _I64, (n,), index)
-    lib = load()
-    fn, kd, vd = _scaled(cache, lib.fa_kv4_write, lib.fa_kv4_write_devscale)
+    lib, at = load(), cache._at
+    fn, (kd, vd) = (lib.fa_kv4_write, cache._descales) if at is None else (lib.fa_kv4_write_devscale, at)
     _call("fa_kv4_write", fn, index, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(),
           cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr(),
           kd, vd, n, heads, d, rows, pages, strides, dt)
@@ -284,13 +276,13 @@ def kv4_read(cache, slot_map, dtype=torch.bfloat16, out=None):
         for name, t in zip(("k", "v"), out):
             if not _is(t, dtype, (n, heads, d), index):
                 _check(name, t, dtype, (n, heads, d), index)
-    lib = load()
-    fn, kd, vd = _scaled(cache, lib.fa_kv4_read, lib.fa_kv4_read_devscale)
+    lib, at = load(), cache._at
+    fn, (kd, vd) = (lib.fa_kv4_read, cache._descales) if at is None else (lib.fa_kv4_read_devscale, at)
     _call("fa_kv4_read", fn, index, cache.k_codes.data_ptr(), cache.k_scales.data_ptr(),
           cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), slot_map.data_ptr(), out[0].data_ptr(),
           out[1].data_ptr(), kd, vd, n, heads, d, rows, pages, _dtype_of("out", out[0]))
     if given is not None:
-        increment_version(given)
+        _written(given)
     return out
 
 
@@ -316,7 +308,8 @@ def paged_attention_kv4(q, cache, cu_seqlens_q, seqused_k, block_table, *, max_s
     need one each.  causal: "none", "top_left" or "bottom_right", as in the
     varlen calls (True says neither and is refused).  There is no gradient:
     queries that require one are refused."""
-    _no_gradients("paged_attention_kv4", q)
+    if q.requires_grad or forward_ad._current_level >= 0:
+        _no_gradients("paged_attention_kv4", q)
     if causal is True:
         raise ValueError('causal=True: say "bottom_right" (the default) or "top_left"')
     dt = _dtype_of("q", q)
@@ -329,12 +322,12 @@ def paged_attention_kv4(q, cache, cu_seqlens_q, seqused_k, block_table, *, max_s
         _check("cu_seqlens_q", cu_seqlens_q, _I32, (n + 1,), index)
         _check("seqused_k", seqused_k, _I32, (n,), index)
         _check("block_table", block_table, _I32, (n, max_pages), index)
-    given = [t for t in (out, lse) if t is not None]
-    if out is None:
+    new_out, new_lse = out is None, lse is None
+    if new_out:
         out = torch.empty_like(q)
     elif not _is(out, q.dtype, (total_q, H, d), index):
         _check("out", out, q.dtype, (total_q, H, d), index)
-    if lse is None:
+    if new_lse:
         lse = torch.empty((H, total_q), dtype=torch.float32, device=q.device)
     elif not _is(lse, torch.float32, (H, total_q), index):
         _check("lse", lse, torch.float32, (H, total_q), index)
@@ -344,14 +337,14 @@ def paged_attention_kv4(q, cache, cu_seqlens_q, seqused_k, block_table, *, max_s
         workspace = paged_attention_kv4_workspace(q, cache, max_seqlen_q=max_seqlen_q, n_seqs=n, total_k=total_k)
     elif workspace.dim() != 1 or not _is(workspace, _U8, workspace.shape, index):
         _check("workspace", workspace, _U8, (None,), index)
-    lib = load()
-    fn, kd, vd = _scaled(cache, lib.fa_fwd_paged_kv4, lib.fa_fwd_paged_kv4_devscale)
+    lib, at = load(), cache._at
+    fn, (kd, vd) = (lib.fa_fwd_paged_kv4, cache._descales) if at is None else (lib.fa_fwd_paged_kv4_devscale, at)
     _call("fa_fwd_paged_kv4", fn, index, q.data_ptr(), cache.k_codes.data_ptr(),
           cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), out.data_ptr(),
           lse.data_ptr(), cu_seqlens_q.data_ptr(), seqused_k.data_ptr(), block_table.data_ptr(), n, max_pages, rows,
           pages, total_q, max_seqlen_q, total_k, H, heads, d, 1.0 / math.sqrt(d) if scale is None else scale,
           CAUSAL[causal] if isinstance(causal, str) else int(causal), dt, kd, vd,
           workspace.data_ptr(), workspace.shape[0])
-    if given:
-        increment_version(given)
+    if not (new_out and new_lse):
+        _written((out, lse))
     return out, lse

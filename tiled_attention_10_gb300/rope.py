@@ -8,7 +8,7 @@ import struct
 import torch
 
 from .binding import FaError, fa_qk_norm_rope_bwd_workspace_size, load
-from .paged import _call, _check, _dtype_of, _I32, _is, _no_tangents, increment_version
+from .paged import _call, _check, _dtype_of, _I32, _is, _no_tangents, _written, forward_ad
 
 _F64 = torch.float64
 
@@ -139,7 +139,7 @@ def _forward(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, pair_axis
           H, H_kv, D, rot, axes, axis, 1 if interleaved else 0, 1 if norm else 0, eps,
           _four_strides(*qs, *ks, *qos, *kos), dt)
     if given is not None:
-        increment_version(given)
+        _written(given)
     return out
 
 
@@ -157,7 +157,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
     """dq, dk, dq_weight, dk_weight of qk_norm_rope from the gradients of its
     outputs and its inputs.  A weight's gradient is None where the forward had no
     such weight, or with weight_grads=False."""
-    _no_tangents("qk_norm_rope_backward", dq_out, dk_out, q, k, q_weight, k_weight, inv_freq)
+    if forward_ad._current_level >= 0:
+        _no_tangents("qk_norm_rope_backward", dq_out, dk_out, q, k, q_weight, k_weight, inv_freq)
     dt = _dtype_of("q", q)
     B, S, H, H_kv, D, bsnd = _sizes(q, k, layout)
     index = q.get_device()
@@ -216,7 +217,8 @@ def qk_norm_rope(q, k, positions=None, inv_freq=None, *, q_weight=None, k_weight
     the norm, inv_freq=None the rotation.  `out`: a pair to write into, which may
     be (q, k) themselves; only where no gradient is asked for.  Gradients of
     inv_freq and forward-mode derivatives (torch.autograd.forward_ad) are refused."""
-    _no_tangents("qk_norm_rope", q, k, q_weight, k_weight, inv_freq)
+    if forward_ad._current_level >= 0:
+        _no_tangents("qk_norm_rope", q, k, q_weight, k_weight, inv_freq)
     if inv_freq is not None and inv_freq.requires_grad and torch.is_grad_enabled():
         raise ValueError("inv_freq has no gradient: detach it")
     wants = torch.is_grad_enabled() and (q.requires_grad or k.requires_grad
