@@ -437,16 +437,19 @@ fa_status_t fa_paged_slots(const int32_t* past_k, const int32_t* new_q, const in
  *   q_weight, k_weight: [D] in `dtype`, or NULL for ones; NULL without `norm`.
  *   positions: int32 [n_axes, B, S], any value of the type; n_axes 1..4.
  *   inv_freq: double [rot_dim / 2], radians a position (a device array).
- *     The angle is reduced modulo a turn in 64-bit integers, so that it is as
- *     exact at position 2^31 as at 1; a frequency that is not finite, or 2^64 and more,
- *     reads as 0.
+ *     The angle is reduced modulo a turn in 64-bit integers: a frequency f is
+ *     held to max(f, 1) 2^-63 turns, so that up to 1 radian a position the angle
+ *     is as exact at position 2^31 as at 1.  A frequency that is not finite, or
+ *     2^64 and more, reads as 0.
  *   pair_axis: HOST array [rot_dim / 2] of axes, each < n_axes; NULL: all 0.
  *   rot_dim: 0 (norm only; positions and inv_freq may be NULL) or a multiple
  *     of 16 up to D.  norm = 0 with rot_dim = 0 is FA_ERR_INVALID_ARG.
- *   dtype: FA_DTYPE_F16 or FA_DTYPE_BF16; D 64 or 128.  fp32 arithmetic, one
- *     rounding.  B * S = 0 returns FA_OK.
+ *   dtype: FA_DTYPE_F16 or FA_DTYPE_BF16; D 64 or 128; H and H_kv up to 2^20
+ *     (FA_ERR_UNSUPPORTED above).  fp32 arithmetic, one rounding.  Elements that
+ *     are not rotated, and not normed, pass as they are.  B * S = 0 returns FA_OK.
  * eps finite and >= 0.  One launch.  (The sum of squares is an fp32 number: a
- * head with bf16 values beyond 1e18 or so has an infinite one, and u = 0.)
+ * head with bf16 values beyond 1e18 or so has an infinite one, and u = 0; one of
+ * values below 1e-23 or so a zero one, which eps has to cover.)
  *
  * fa_qk_norm_rope_bwd -- its gradients.  With g = dy turned back, r =
  * rsqrt(mean(x^2) + eps), h = x r:
@@ -490,7 +493,8 @@ fa_status_t fa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const vo
  * The head is outside the row so that the rows of one head of one page, what an
  * attention work item reads, are one run of memory.  A scale's NaN code, which
  * fa_kv4_write never makes, reads as NaN (and may reach the neighbours of the
- * sequence that holds it); nothing else makes a value NaN or infinite.
+ * sequence that holds it); nothing else makes a value NaN, or infinite but past
+ * the range of f16 where that is the type asked for.
  * descale_k, descale_v are host floats in [2^-100, 2^100] (FA_ERR_INVALID_ARG
  * outside).  The calls named _devscale take them as device pointers instead (one
  * fp32 each, 4-byte aligned, NULL for 1.0) and read them when they run, so that a
@@ -543,17 +547,20 @@ fa_status_t fa_kv4_read_devscale(const uint8_t* k_codes, const uint8_t* k_scales
  * fa_fwd_paged_kv4 -- attention of packed queries over the 4-bit cache: q, o,
  *   lse, cu_seqlens_q, seqused_k, block_table, causal and a row without keys
  *   (O = 0, lse = -inf) as fa_fwd_paged; the cache and its descales as above.
- *   dtype: F16 or BF16 (of q and o, which must not overlap).  Keys behind seqused_k are not looked at;
- *   pages outside [0, num_pages) read as zeros.
+ *   dtype: F16 or BF16 (of q and o, which must not overlap).  Keys behind
+ *   seqused_k are not looked at; pages outside [0, num_pages) read as zeros.
  *   Where max_seqlen_q * H / H_kv is small (at most 128: decoding, speculative
  *   tokens; at most 512 where total_k >= 2048 n_seqs) the cache is read as it
  *   is, its work split evenly over the GPU whatever the lengths; otherwise the
  *   keys and values of the sequences that bring queries are unpacked into the
  *   workspace (exactly: code * scale fits both types) and the packed
- *   tensor-core forward reads them there.
+ *   tensor-core forward reads them there.  The first way holds probabilities in
+ *   f16 for both types, the second in `dtype` (for bf16 8 times coarser, as
+ *   fa_fwd_varlen): max_seqlen_q and total_k decide.
+ *   scale * descale_k has to be finite.
  *   total_k: at least the sum of seqused_k (host-known; it sizes the unpacked
- *   rows; keys past it may be left out).  At most 16384 sequences when
- *   unpacking.
+ *   rows, and keys past it may be left out; and it decides as above).  At most
+ *   16384 sequences when unpacking.
  *   workspace: at least fa_fwd_paged_kv4_workspace_size bytes, 256-byte
  *   aligned, contents irrelevant; one of that size serves any call with at
  *   most as many sequences, queries and keys.  Two launches; calls sharing a

@@ -784,7 +784,7 @@ def test_sequences_up_to_two_billion_keys(cuda_lib, qn, ps, rest):
     # one add and 8 products.
     steps = n / 32 / 1824 if qn * 8 <= 16 else n / 128 / 152
     sums, products = (4 * steps, 2 * steps) if qn * 8 <= 16 else (steps, 8 * steps)
-    bo, bl = ref.attend_bounds(O, PV, A, ps, 64, torch.bfloat16, 2.0 ** -12, 0.0)
+    bo, bl = ref.attend_bounds(O, PV, A, ps, 64, torch.bfloat16, ref.half_step(torch.float16), 0.0)
     loss, share = sums * 2.0 ** -24, 2.0 * ps / n
     assert (np.abs(np64(o) - O) <= bo + (loss + products * 2.0 ** -23 + share) * (PV + np.abs(O))).all()
     assert (np.abs(np64(lse) - (L + np.log(n / ps))) <= bl + loss + share + 2.0 ** -24 * 22).all()

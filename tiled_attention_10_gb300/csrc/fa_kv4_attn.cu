@@ -20,9 +20,10 @@
  * changes from S^T's accumulator layout to an operand by one 8x8 transposition
  * (movmatrix) for 8 keys.
  *   codes -> f16: cvt e2m1x2 (exact), times the group's scale (exact: 2 x 4
- *   significant bits); bf16 queries become f16 exactly too, each row shifted
- *   by a power of two that its scale takes back.  P in f16 is the only
- *   rounding: 2^-12 of each probability; scores, sums and O are fp32.
+ *   significant bits); bf16 queries become f16 too, each row shifted by a power
+ *   of two that its scale takes back: exactly, but for elements below 2^-22 of
+ *   the row's largest, which keep fewer bits.  Beside that P in f16 is the only
+ *   rounding: 2^-11 of each probability; scores, sums and O are fp32.
  * Work: every sequence's keys, times its heads, are one line of 64-key chunks,
  * cut into equal runs for the resident blocks whatever the lengths are; a
  * (sequence, head) that a cut divides leaves fp32 partials that a second
@@ -32,8 +33,11 @@
  * More rows (17 to 128, to 512 over long sequences): fa_kv4_wide.cu.
  *
  * Many rows (chunked prefill): bound by the matrix products.  The keys and
- * values are unpacked once into a 16-bit workspace (a few per cent of the
- * time), exactly, and the tcgen05 forward of packed sequences reads them there.
+ * values are unpacked once into a 16-bit workspace (a tenth of the time),
+ * exactly, and the tcgen05 forward of packed sequences reads them there.  That
+ * one holds P in the queries' type, as everywhere in this library: a rounding of
+ * 2^-8 of each probability for bf16, of 2^-11 for f16 (2^-25 of the row's largest
+ * for those below 2^-14 of it).
  */
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -192,8 +196,9 @@ __device__ __forceinline__ void load_step(const AttnParams& p, const Lane& me, u
 template <int D, int NT>
 struct Cfg {
   static constexpr int kRows = 8 * NT;
-  // Warps of a block and resident blocks an SM: 12 warps of 168 registers (O and
-  // the ring grow with the rows).  With 8 rows, 128 sequences of 8192 keys (floor 178 us): 4 blocks of 3 warps 210 us, 2 x 8
+  // Warps of a block and resident blocks an SM: 12 warps of up to 168 registers
+  // (8 rows use 144, 130 at D = 64; 16 rows 160 at 64, and at 128 all 168 with 12
+  // bytes spilled).  With 8 rows, 128 sequences of 8192 keys (floor 178 us): 4 blocks of 3 warps 210 us, 2 x 8
   // (128 registers) 214, 6 x 2 211, 2 x 4 224; 4000 of 256 keys, where units
   // end often: 383, 557, 354, 525; one of 65536: 28, 26, 32, 27.
   static constexpr int kWarps = NT == 1 ? 3 : 4;
@@ -684,12 +689,15 @@ __global__ void __launch_bounds__(kUnpackThreads) fa_kv4_unpack_kernel(const __g
 // mma.sync operands, up to which it is unpacked on the way to tcgen05, and up to
 // which it is so where the sequences are long (total_k a sequence): a workspace
 // of 16-bit rows costs what it writes and reads, a 128-row tile its unpacking.
-// us, tiles / workspace, D 128, H 32 / 8: 128 sequences of 8192 keys 32 rows 449
-// (506 in mma.sync operands), 64 rows 455, 128 rows 479 / 1554, 256 rows
-// 920 / 1600, 512 rows 1833 / 2298; 32 of 2048 256 rows 104 / 132, 512 rows
-// 173 / 195; 8 of 2048 256 rows 48 / 47, 512 rows 66 / 52; one of 65536 256
-// rows 100 / 690, 512 rows 142 / 699; 256 of 256 128 rows 133 / 152, 256 rows
-// 239 / 165.
+// us, tiles / workspace, D 128, H 32 / 8:
+//   128 sequences of 8192 keys: 16 rows 294, 32 rows 458 (506 in mma.sync operands),
+//     64 rows 456, 128 rows 477 / 1575, 256 rows 919 / 1628, 512 rows 1816 / 2305
+//   32 of 2048: 256 rows 104 / 142, 512 rows 175 / 197
+//   8 of 2048: 256 rows 48 / 50, 512 rows 66 / 51 (few units: the rule takes the
+//     slower way here)
+//   one of 65536: 256 rows 101 / 687, 512 rows 142 / 691
+//   256 of 256: 128 rows 133 / 152, 256 rows 242 / 165
+// The rule goes by total_k, the caller's bound on all keys, and so by the mean.
 constexpr int64_t kNarrowRows = 16, kStreamRows = 128, kLongStreamRows = 512, kLongKeys = 2048;
 bool streams(int64_t rows, int64_t n_seqs, int64_t total_k) {
   return rows <= (total_k / kLongKeys >= n_seqs ? kLongStreamRows : kStreamRows);

@@ -7,15 +7,18 @@
  * the products', and mma.sync straight from registers serves (fa_kv4_attn.cu).
  * From 17 rows on its products and registers cost more than that, while here a
  * block costs nearly the same for any number of rows up to 128.  Measured with
- * 128 sequences of 8192 keys (H_kv 8, D 128): 449 us with 32 rows, 479 with 128
- * (1.15 PFLOP/s); HBM alone would take 178.  A block takes 2000 cycles: the
- * softmax warps (one a sub-partition, a row of 128 scores a thread) are busy all
- * of them, the issue of the 16 products and its waits about 1600, an unpacking
- * warp about 1100.  In pairs of fp32 (f32x2) the softmax took the kernel from
- * 512 us to 460; a page looked up without a branch around it, 450; the next
- * unit's first rows loaded while a unit ends, 336 us for 1000 sequences of 256
+ * 128 sequences of 8192 keys (H_kv 8, D 128): 458 us with 32 rows, 477 with 128
+ * (1.15 PFLOP/s); HBM alone would take 178.  D = 64, 256 such sequences: 787 us.
+ * A block takes 2000 cycles: the softmax warps are busy all of them (a row of 128
+ * scores a thread, so that 32 rows are one warp's, on one of four sub-partitions),
+ * the issue of the 16 products and its waits about 1600, an unpacking warp about
+ * 1100.  What each step gave when it was made: the softmax in pairs of fp32
+ * (f32x2) 512 us to 460; a page looked up without a branch around it, 450; the
+ * next unit's first rows loaded while a unit ends, 336 us for 1000 sequences of 256
  * keys instead of 346 (12,000 cycles a unit of two blocks, most of them one
- * latency after another: Q, S, softmax twice, output).  Tried and
+ * latency after another: Q, S, softmax twice, output).  The schedule hangs on
+ * small things: where the scale comes from moves it by 1 to 2 % (451 us as a
+ * launch parameter, 457 from shared memory).  Tried and
  * slower: P against the maximum so far with a check behind it (550), two softmax
  * warpgroups, on alternate blocks (487) or on half of each block's keys (457, 501
  * with 128 rows; faster at D = 64, 702 for 256 sequences against 788),

@@ -8,7 +8,7 @@
  * bisection; so one launch does all, with no pass that others wait for.  New
  * entries are taken from the free list by the blocks that need them, never
  * from the table another block is writing.  Latency is what counts: a few loads
- * one after another, 5.2 us for 128 requests of a token, 6.5 for 32 of 2000 (the
+ * one after another, 5.4 us for 128 requests of a token, 6.4 for 32 of 2000 (the
  * sums of 16384 requests cost a block 128 KB of L2 reads).
  */
 #include <cuda_runtime.h>
