@@ -804,3 +804,41 @@ def test_no_descales_are_ones(cuda_lib):
     assert binding.fa_kv4_read_devscale(*ptrs, slots.data_ptr(), k.data_ptr(), v.data_ptr(), None, None, 20, 1, 64, 16, 2, "f16",
                                         stream) == 0
     assert all(torch.equal(s, t) for s, t in zip(fa.kv4_read(a, slots, torch.float16), (k, v)))
+
+
+def test_queries_past_32_bit_offsets(cuda_lib):
+    """300,000 requests of one token each: rows of q and O, and of the table, far beyond 2^32 bytes."""
+    n, H, D = 300_000, 64, 128
+    g = torch.Generator().manual_seed(51)
+    cache = fa.KV4Cache.allocate(3, 16, 8, D, k_descale=0.003, v_descale=0.002)
+    rows = [torch.randn(48, 8, D, generator=g).bfloat16().cuda() for _ in range(2)]
+    fa.kv4_write(*rows, torch.arange(48, device="cuda"), cache)
+    q = torch.randn(n, H, D, generator=torch.Generator(device="cuda").manual_seed(52), device="cuda", dtype=torch.bfloat16)
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    used = torch.arange(n, dtype=torch.int32, device="cuda") % 33
+    table = (torch.arange(2 * n, dtype=torch.int32, device="cuda") % 3).view(n, 2).contiguous()
+    used.clamp_(max=32)
+    o, lse = fa.paged_attention_kv4(q, cache, cu, used, table, max_seqlen_q=1, total_k=32 * n)
+    for a in (0, 140_000, n - 70):
+        part = slice(a, a + 70)
+        o2, l2 = fa.paged_attention_kv4(q[part].contiguous(), cache, cu[:71].contiguous(), used[part].contiguous(), table[part].contiguous(),
+                                        max_seqlen_q=1, total_k=32 * 70)
+        # one chunk of keys each: no request is cut, whatever the split of the work
+        assert torch.equal(o[part], o2) and torch.equal(lse[:, part], l2)
+
+
+def test_write_rows_far_apart(cuda_lib):
+    """Token and head strides that pass 2^32 elements."""
+    g = torch.Generator().manual_seed(53)
+    near = [torch.randn(3, 2, 64, generator=g).half().cuda() for _ in range(2)]
+    step = (1 << 32) + 64
+    buf = torch.empty(2 * step + 4096, dtype=torch.float16, device="cuda")
+    far = buf.as_strided((3, 2, 64), (step, 1024, 1))
+    wide = buf.as_strided((3, 2, 64), (512, step, 1), 2048)
+    slots = torch.arange(3, device="cuda")
+    for view in (far, wide):
+        a, b = junk_cache(1, 16, 2, 64, 0.003, 0.002), junk_cache(1, 16, 2, 64, 0.003, 0.002)
+        view.copy_(near[0])
+        fa.kv4_write(view, view, slots, a)
+        fa.kv4_write(near[0], near[0], slots, b)
+        assert all(torch.equal(x, y) for x, y in zip(cache_bits(a), cache_bits(b)))

@@ -305,3 +305,18 @@ def test_frequencies_from_2_to_the_64_on_read_as_zero(cuda_lib):
     assert all(torch.equal(a, b) for a, b in zip(fa.qk_norm_rope(q, k, pos, big, norm=False, layout="BSND"), (q, k)))
     below = torch.nextafter(big[0], big[0] * 0).expand(8).contiguous()
     assert not torch.equal(fa.qk_norm_rope(q, k, pos, below, norm=False, layout="BSND")[0], q)
+
+
+def test_strides_past_32_bits(cuda_lib):
+    """Rows of q and k, and of the outputs, more than 2^32 elements apart, both ways."""
+    q, k, w, pos, freq, axis, d = make(1, 3, 2, 2, 64, 64, 1, "BSND", "bf16", 15)
+    step = (1 << 32) + 64
+    buf = torch.empty(2 * step + (1 << 20), dtype=torch.bfloat16, device="cuda")
+    far = [buf.as_strided((1, 3, 2, 64), (8, step, 512, 1), 4096 * i) for i in range(4)]
+    for a, b in zip(far, (q, k, *d)):
+        a.copy_(b)
+    kw = dict(q_weight=w[0], k_weight=w[1], layout="BSND")
+    want, grads = fa.qk_norm_rope(q, k, pos, freq, **kw), fa.qk_norm_rope_backward(*d, q, k, pos, freq, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(grads, fa.qk_norm_rope_backward(far[2], far[3], far[0], far[1], pos, freq, **kw)))
+    fa.qk_norm_rope(far[0], far[1], pos, freq, out=(far[2], far[3]), **kw)
+    assert torch.equal(far[2], want[0]) and torch.equal(far[3], want[1])

@@ -198,9 +198,10 @@ struct Cfg {
   static constexpr int kRows = 8 * NT;
   // Warps of a block and resident blocks an SM: 12 warps of up to 168 registers
   // (8 rows use 144, 130 at D = 64; 16 rows 160 at 64, and at 128 all 168 with 12
-  // bytes spilled).  With 8 rows, 128 sequences of 8192 keys (floor 178 us): 4 blocks of 3 warps 210 us, 2 x 8
-  // (128 registers) 214, 6 x 2 211, 2 x 4 224; 4000 of 256 keys, where units
-  // end often: 383, 557, 354, 525; one of 65536: 28, 26, 32, 27.
+  // bytes spilled).  With 8 rows, 128 sequences of 8192 keys (floor 178 us):
+  // 4 blocks of 3 warps 210 us, 2 x 8 (128 registers) 214, 6 x 2 211, 2 x 4 224;
+  // 4000 of 256 keys, where units end often: 383, 557, 354, 525; one of 65536:
+  // 28, 26, 32, 27.
   static constexpr int kWarps = NT == 1 ? 3 : 4;
   static constexpr int kBlocks = NT == 1 ? 4 : 3;
   // A warp's ring: three stages; at the end of a unit its O lies in the third
